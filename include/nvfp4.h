@@ -388,6 +388,53 @@ nvfp4_status nvfp4_mxfp8_gemm(const uint8_t* a, const uint8_t* sfa, const uint8_
 
 /*
  * ------------------------------------------------------------------------
+ * MXFP4 variant (Open Compute Project microscaling, the 4-bit sibling of
+ * MXFP8): E2M1 elements, one E8M0 scale (2^(byte - 127)) per 32 elements
+ * along K, no per-tensor scale.
+ *   codes   [rows, K/2] uint8, packed as NVFP4's (element 2j in bits 0-3)
+ *   scales  nvfp4_mxfp4_sf_bytes(rows, K) bytes, laid out as MXFP8's
+ * ------------------------------------------------------------------------
+ */
+
+/* Size of the swizzled MXFP4 scale buffer: ceil(rows/128)*128 *
+ * ceil(k/128)*4.  0 if rows < 1 or k < 32 or k % 32 != 0.  Host-only. */
+size_t nvfp4_mxfp4_sf_bytes(int64_t rows, int64_t k);
+
+/*
+ * bf16 -> MXFP4.  For each row and each 32-element block along K:
+ *     amax = max |x_i|
+ *     amax == 0:  scale byte 0;  codes E2M1(x_i) (zeros, sign kept)
+ *     else        s = clamp(floor(log2 amax) - 2, -127, 127);  scale byte s + 127
+ *                 code_i = E2M1_satfinite(fl(x_i * 2^-s))   (RNE, +-6)
+ * (2 is the exponent of E2M1's largest normal, 6 = 1.5 * 2^2, so the block
+ * maximum scales into [4, 8) and what lies above 6 saturates).
+ *   x      [M, K] bf16, finite
+ *   codes  [M, K/2] uint8, written;  sf  nvfp4_mxfp4_sf_bytes(M, K), written
+ *          including its zero padding.
+ * M >= 1, K % 64 == 0.  Errors: EINVAL, EALIGN, EARCH, ECUDA.
+ */
+nvfp4_status nvfp4_mxfp4_quantize(const void* x, int64_t M, int64_t K,
+                                  uint8_t* codes, uint8_t* sf, void* stream);
+
+/*
+ * Block-scaled MXFP4 GEMM on the tensor cores (tcgen05, kind::mxf4, one E8M0
+ * scale per 32 elements), dequant folded into the epilogue:
+ *     y[m, n] = bf16_rn( alpha * sum_k a_hat[m,k] * b_hat[n,k] + bias[n] )
+ * with a_hat = e2m1(a) * 2^(sfa - 127), b_hat likewise; the sum in fp32.
+ *   a  [M, K/2] codes, sfa nvfp4_mxfp4_sf_bytes(M, K);  b [N, K/2] codes (the
+ *   weight, PyTorch [out, in]), sfb nvfp4_mxfp4_sf_bytes(N, K);
+ *   alpha finite (1 for a plain MXFP4 layer);  bias [N] bf16 or NULL;
+ *   y [M, N] bf16, written.
+ * Tile shape and K split as nvfp4_gemm's (nvfp4_gemm_plan reports them).
+ * M >= 1, N >= 8 with N % 8 == 0, K % 64 == 0.  Errors: EINVAL, EALIGN,
+ * EARCH, ECUDA; a barrier time-out records NVFP4_ETIMEOUT (nvfp4_check_fault).
+ */
+nvfp4_status nvfp4_mxfp4_gemm(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
+                              const uint8_t* sfb, int64_t M, int64_t N, int64_t K,
+                              float alpha, const void* bias, void* y, void* stream);
+
+/*
+ * ------------------------------------------------------------------------
  * Row-wise FP8 (W8A8) variant (BFL doc, `fp8r` bullet and "Kernels" row
  * `fp8r`: an E4M3 `weight` with one fp32 `weight_scale` per row;
  * activations quantized to E4M3 row by row at run time; the GEMM applies the

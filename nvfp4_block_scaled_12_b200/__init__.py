@@ -72,6 +72,10 @@ def _load() -> ctypes.CDLL:
     lib.nvfp4_mxfp8_sf_bytes.restype = ctypes.c_size_t
     lib.nvfp4_mxfp8_quantize.argtypes = [vp, i64, i64, vp, vp, vp]
     lib.nvfp4_mxfp8_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, f32, vp, vp, vp]
+    lib.nvfp4_mxfp4_sf_bytes.argtypes = [i64, i64]
+    lib.nvfp4_mxfp4_sf_bytes.restype = ctypes.c_size_t
+    lib.nvfp4_mxfp4_quantize.argtypes = [vp, i64, i64, vp, vp, vp]
+    lib.nvfp4_mxfp4_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, f32, vp, vp, vp]
     lib.nvfp4_fp8row_quantize.argtypes = [vp, i64, i64, vp, vp, vp]
     lib.nvfp4_fp8row_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp, vp]
     lib.nvfp4_dequantize.argtypes = [vp, vp, f32, i64, i64, vp, vp]
@@ -86,7 +90,8 @@ def _load() -> ctypes.CDLL:
                  "nvfp4_mxfp8_quantize", "nvfp4_mxfp8_gemm", "nvfp4_fp8row_quantize", "nvfp4_fp8row_gemm",
                  "nvfp4_dequantize", "nvfp4_check_fault", "nvfp4_gemm_tile_shape", "nvfp4_gemm_scaled",
                  "nvfp4_gemm_quant_scaled", "nvfp4_testing_set_grid_wait", "nvfp4_w4a16_gemm",
-                 "nvfp4_gemm_plan", "nvfp4_gemm_amax", "nvfp4_quantize_from_amax"):
+                 "nvfp4_gemm_plan", "nvfp4_gemm_amax", "nvfp4_quantize_from_amax", "nvfp4_mxfp4_quantize",
+                 "nvfp4_mxfp4_gemm"):
         getattr(lib, name).restype = ctypes.c_int
     lib.nvfp4_last_error.argtypes = []
     lib.nvfp4_last_error.restype = ctypes.c_char_p
@@ -196,6 +201,19 @@ def nvfp4_mxfp8_quantize(x: int, M: int, K: int, codes: int, sf: int, stream: in
 def nvfp4_mxfp8_gemm(a: int, sfa: int, b: int, sfb: int, M: int, N: int, K: int, alpha: float, bias: int, y: int,
                      stream: int) -> None:
     _check(library().nvfp4_mxfp8_gemm(a, sfa, b, sfb, M, N, K, alpha, bias or None, y, stream))
+
+
+def nvfp4_mxfp4_sf_bytes(rows: int, k: int) -> int:
+    return int(library().nvfp4_mxfp4_sf_bytes(rows, k))
+
+
+def nvfp4_mxfp4_quantize(x: int, M: int, K: int, codes: int, sf: int, stream: int) -> None:
+    _check(library().nvfp4_mxfp4_quantize(x, M, K, codes, sf, stream))
+
+
+def nvfp4_mxfp4_gemm(a: int, sfa: int, b: int, sfb: int, M: int, N: int, K: int, alpha: float, bias: int, y: int,
+                     stream: int) -> None:
+    _check(library().nvfp4_mxfp4_gemm(a, sfa, b, sfb, M, N, K, alpha, bias or None, y, stream))
 
 
 def nvfp4_fp8row_quantize(x: int, M: int, K: int, codes: int, scale: int, stream: int) -> None:
@@ -450,6 +468,60 @@ def gemm_mxfp8(a: MXFP8Tensor, b: MXFP8Tensor, bias=None, alpha: float = 1.0, y=
         y = torch.empty(M, N, dtype=torch.bfloat16, device=a.codes.device)
     _need(y, torch.bfloat16, (M, N), "y", dev=dev)
     nvfp4_mxfp8_gemm(_ptr(a.codes), _ptr(a.sf), _ptr(b.codes), _ptr(b.sf), M, N, K, float(alpha), _ptr(bias),
+                     _ptr(y), _stream(stream))
+    return y
+
+
+@dataclass
+class MXFP4Tensor:
+    """A [rows, k] MXFP4 tensor on the GPU: E2M1 codes (two per byte) and
+    swizzled E8M0 scales (one per 32 elements)."""
+    codes: "object"   # uint8 [rows, k/2]
+    sf: "object"      # uint8 [nvfp4_mxfp4_sf_bytes(rows, k)]
+    rows: int
+    k: int
+
+
+def _need_mxfp4(t, name, rows=None, k=None, dev=None):
+    rows = t.rows if rows is None else rows
+    k = t.k if k is None else k
+    torch = _torch()
+    if (t.rows, t.k) != (rows, k):
+        raise ValueError(f"{name} is [{t.rows}, {t.k}], [{rows}, {k}] needed")
+    _need(t.codes, torch.uint8, None, f"{name}.codes", rows * k // 2, dev=dev)
+    _need(t.sf, torch.uint8, None, f"{name}.sf", nvfp4_mxfp4_sf_bytes(rows, k), dev=dev)
+
+
+def quantize_mxfp4(x, out: Optional[MXFP4Tensor] = None, stream=None) -> MXFP4Tensor:
+    """Quantize bf16 ``x`` [M, K] to MXFP4 (power-of-two block scales)."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    M, K = x.shape
+    _need(x, torch.bfloat16, None, "x", dev=dev)
+    if out is None:
+        out = MXFP4Tensor(torch.empty(M, K // 2, dtype=torch.uint8, device=x.device),
+                          torch.empty(nvfp4_mxfp4_sf_bytes(M, K), dtype=torch.uint8, device=x.device), M, K)
+    else:
+        _need_mxfp4(out, "out", M, K, dev=dev)
+    nvfp4_mxfp4_quantize(_ptr(x), M, K, _ptr(out.codes), _ptr(out.sf), _stream(stream))
+    return out
+
+
+def gemm_mxfp4(a: MXFP4Tensor, b: MXFP4Tensor, bias=None, alpha: float = 1.0, y=None, stream=None):
+    """y = bf16(alpha * a_hat @ b_hat^T + bias) for MXFP4 operands."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    if a.k != b.k:
+        raise ValueError("K mismatch")
+    M, N, K = a.rows, b.rows, a.k
+    _need_mxfp4(a, "a", dev=dev)
+    _need_mxfp4(b, "b", dev=dev)
+    if bias is not None:
+        _need(bias, torch.bfloat16, (N,), "bias", dev=dev)
+    if y is None:
+        y = torch.empty(M, N, dtype=torch.bfloat16, device=a.codes.device)
+    _need(y, torch.bfloat16, (M, N), "y", dev=dev)
+    nvfp4_mxfp4_gemm(_ptr(a.codes), _ptr(a.sf), _ptr(b.codes), _ptr(b.sf), M, N, K, float(alpha), _ptr(bias),
                      _ptr(y), _stream(stream))
     return y
 

@@ -196,15 +196,16 @@ bool product_ok(float g_a, float g_b) {
 
 // Checks shared by the two GEMM entry points; fills the operand part of p
 // and the operand tensor maps.
+// mx4: MXFP4 operands, E2M1 codes as NVFP4's with E8M0 scales per 32.
 // mx: 8-bit operands (one E4M3 byte per element), with E8M0 scales per 32
 // (MXFP8) or, with row, one fp32 scale per row passed as sfa / sfb.
-// y (bf16 [M, N]) non-null: the plain NVFP4 epilogue, which may split K
+// split_y (bf16 [M, N]) non-null: the plain NVFP4 or MXFP4 epilogue, which may split K
 // across a cluster (gemm_plan) and then writes y directly from the cluster's
 // reduction.
 nvfp4_status gemm_common(const uint8_t* a, const uint8_t* sfa, const uint8_t* b, const uint8_t* sfb, int64_t M,
                          int64_t N, int64_t K, float alpha, const void* bias, GemmParams* p, GemmTensorMaps* maps,
                          GemmConfig* cfg, const DeviceInfo** dev, bool mx = false, bool row = false,
-                         bool fused = false, void* split_y = nullptr) {
+                         bool fused = false, void* split_y = nullptr, bool mx4 = false) {
   if (!a || !sfa || !b || !sfb) return fail(NVFP4_EINVAL, "null operand pointer");
   nvfp4_status st = check_rows_k("M", M, "K", K);
   if (st != NVFP4_OK) return st;
@@ -261,8 +262,8 @@ nvfp4_status gemm_common(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
     return NVFP4_OK;
   }
   // scale atoms per 128-row block, and atoms per k-tile
-  const int64_t atoms = mx ? (K / 32 + 3) / 4 : K / 64;
-  const uint32_t box_atoms = mx ? 1u : 4u;
+  const int64_t atoms = (mx || mx4) ? (K / 32 + 3) / 4 : K / 64;
+  const uint32_t box_atoms = mx ? 1u : (mx4 ? 2u : 4u);
   st = make_sf_tmap(&maps->sfa, sfa, M, atoms, box_atoms, 1, "A scales");
   if (st != NVFP4_OK) return st;
   // 128-row scale blocks one B tile can touch: a width that is not a
@@ -395,6 +396,44 @@ nvfp4_status nvfp4_mxfp8_gemm(const uint8_t* a, const uint8_t* sfa, const uint8_
   if (st != NVFP4_OK) return st;
   cudaError_t e = launch_gemm(maps, p, cg, false, true, static_cast<cudaStream_t>(stream), *dev);
   if (e != cudaSuccess) return cuda_fail(e, "mxfp8 gemm launch");
+  return ok();
+}
+
+size_t nvfp4_mxfp4_sf_bytes(int64_t rows, int64_t k) { return nvfp4_mxfp8_sf_bytes(rows, k); }
+
+nvfp4_status nvfp4_mxfp4_quantize(const void* x, int64_t M, int64_t K, uint8_t* codes, uint8_t* sf, void* stream) {
+  if (!x || !codes || !sf) return fail(NVFP4_EINVAL, "null pointer");
+  if (check_rows_k("M", M, "K", K) != NVFP4_OK) return NVFP4_EINVAL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(sf))
+    return fail(NVFP4_EALIGN, "pointers must be 16-byte aligned");
+  const DeviceInfo* dev = nullptr;
+  nvfp4_status st = current_device(&dev);
+  if (st != NVFP4_OK) return st;
+  CUtensorMap tx;
+  const int tile_rows = quantize_tile_rows(M, K, dev->num_sms);
+  st = make_tmap(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, K, M, K * 2, 64, static_cast<uint32_t>(tile_rows),
+                 CU_TENSOR_MAP_SWIZZLE_128B, "x");
+  if (st != NVFP4_OK) return st;
+  cudaError_t e = launch_quantize_mxfp4(tx, tile_rows, M, K, codes, sf, static_cast<cudaStream_t>(stream), *dev);
+  if (e != cudaSuccess) return cuda_fail(e, "mxfp4 quantize launch");
+  return ok();
+}
+
+nvfp4_status nvfp4_mxfp4_gemm(const uint8_t* a, const uint8_t* sfa, const uint8_t* b, const uint8_t* sfb, int64_t M,
+                              int64_t N, int64_t K, float alpha, const void* bias, void* y, void* stream) {
+  if (!y) return fail(NVFP4_EINVAL, "null output pointer");
+  if (!aligned16(y)) return fail(NVFP4_EALIGN, "y must be 16-byte aligned");
+  GemmParams p;
+  GemmTensorMaps maps;
+  GemmConfig cg;
+  const DeviceInfo* dev = nullptr;
+  nvfp4_status st =
+      gemm_common(a, sfa, b, sfb, M, N, K, alpha, bias, &p, &maps, &cg, &dev, false, false, false, y, true);
+  if (st != NVFP4_OK) return st;
+  st = make_tmap(&maps.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, "Y");
+  if (st != NVFP4_OK) return st;
+  cudaError_t e = launch_gemm_mxfp4(maps, p, cg, static_cast<cudaStream_t>(stream), *dev);
+  if (e != cudaSuccess) return cuda_fail(e, "mxfp4 gemm launch");
   return ok();
 }
 

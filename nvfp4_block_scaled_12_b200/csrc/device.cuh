@@ -139,6 +139,23 @@ __device__ __forceinline__ uint32_t bf16x2_absmax(uint32_t acc, uint32_t w) {
   return __vmaxu2(acc, __vminu2(w & 0x7FFF7FFFu, 0x7F807F80u));
 }
 
+// Shared exponent of a 32-element microscaling block whose largest magnitude
+// is amax: clamp(floor(log2 amax) - emax, -127, 127), -127 for amax == 0, with
+// emax the exponent of the element format's largest normal.  inv = 2^-s.
+__device__ __forceinline__ int mx_block_exponent(float amax, int emax, float& inv) {
+  const uint32_t bits = __float_as_uint(amax);
+  int e;  // floor(log2(amax)) for amax > 0
+  if (bits >= 0x00800000u)
+    e = static_cast<int>(bits >> 23) - 127;
+  else
+    e = (31 - __clz(static_cast<int>(bits))) - 149;  // fp32 subnormal: bits * 2^-149
+  int s = bits == 0u ? -127 : e - emax;
+  s = s < -127 ? -127 : (s > 127 ? 127 : s);
+  // 2^-s exactly: a normal float for s <= 126, the subnormal 2^-127 for s = 127
+  inv = s <= 126 ? __uint_as_float(static_cast<uint32_t>(127 - s) << 23) : __uint_as_float(0x00400000u);
+  return s;
+}
+
 // MXFP8 block (OCP microscaling): 32 fp32 values (exactly representable in
 // bf16) -> 32 E4M3 bytes in 8 little-endian words and the E8M0 scale byte.
 //   amax == 0: scale byte 0 (2^-127);  else s = clamp(floor(log2 amax) - 8,
@@ -147,16 +164,8 @@ __device__ __forceinline__ uint32_t quantize_mx_block32(const float (&v)[32], ui
   float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
-  const uint32_t bits = __float_as_uint(amax);
-  int e;  // floor(log2(amax)) for amax > 0
-  if (bits >= 0x00800000u)
-    e = static_cast<int>(bits >> 23) - 127;
-  else
-    e = (31 - __clz(static_cast<int>(bits))) - 149;  // fp32 subnormal: bits * 2^-149
-  int s = bits == 0u ? -127 : e - 8;
-  s = s < -127 ? -127 : (s > 127 ? 127 : s);
-  // 2^-s exactly: a normal float for s <= 126, the subnormal 2^-127 for s = 127
-  const float inv = s <= 126 ? __uint_as_float(static_cast<uint32_t>(127 - s) << 23) : __uint_as_float(0x00400000u);
+  float inv;
+  const int s = mx_block_exponent(amax, 8, inv);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     uint16_t lo, hi;
@@ -166,6 +175,25 @@ __device__ __forceinline__ uint32_t quantize_mx_block32(const float (&v)[32], ui
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(__fmul_rn(v[4 * i + 3], inv)),
         "f"(__fmul_rn(v[4 * i + 2], inv)));
     w[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+  }
+  return static_cast<uint32_t>(s + 127);
+}
+
+// MXFP4 block (OCP microscaling): 32 fp32 values (exactly representable in
+// bf16) -> 32 E2M1 codes in 4 little-endian words and the E8M0 scale byte.
+//   amax == 0: scale byte 0 (2^-127);  else s = clamp(floor(log2 amax) - 2,
+//   -127, 127), scale byte s + 127;  code_i = E2M1_satfinite(fl(v_i * 2^-s)).
+__device__ __forceinline__ uint32_t quantize_mxfp4_block32(const float (&v)[32], uint32_t (&w)[4]) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  float inv;
+  const int s = mx_block_exponent(amax, 2, inv);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float* p = v + 8 * i;
+    w[i] = e2m1x8_from_f32(__fmul_rn(p[0], inv), __fmul_rn(p[1], inv), __fmul_rn(p[2], inv), __fmul_rn(p[3], inv),
+                           __fmul_rn(p[4], inv), __fmul_rn(p[5], inv), __fmul_rn(p[6], inv), __fmul_rn(p[7], inv));
   }
   return static_cast<uint32_t>(s + 127);
 }
@@ -527,6 +555,29 @@ __device__ __forceinline__ void tc_mma_nvf4_pair(uint32_t d_tmem, uint64_t adesc
       : "memory");
 }
 
+// D (TMEM, fp32) (+)= A * B with MXFP4 operands: E2M1 elements from shared
+// memory and one E8M0 scale per 32 elements from TMEM, K = 64: the MMA reads
+// two of the four scales of a TMEM scale word, named (as byte 0 or 2) in the
+// descriptor and in the top two bits of the scale addresses.
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                 uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+
 // Shared-memory matrix descriptor, K-major operand rows of 128 bytes with the
 // 128-byte swizzle; groups of 8 rows are 1024 bytes apart.
 __device__ __forceinline__ uint64_t sdesc_kmajor_sw128(uint32_t saddr) {
@@ -545,6 +596,13 @@ __host__ __device__ constexpr uint32_t idesc_nvf4(int m, int n) {
          | (1u << 10)                               // B format: E2M1
          | (static_cast<uint32_t>(n >> 3) << 17)    // N / 8
          | (static_cast<uint32_t>(m >> 4) << 24);   // M / 16 (scale format bit 23 = 0: UE4M3)
+}
+
+// Instruction descriptor of the MXFP4 block-scaled MMA: as NVFP4's with UE8M0
+// scales; sf_id (0 or 2) is the first of the two scale bytes this MMA reads,
+// for A (bits 29-30) and B (bits 4-5).
+__host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, uint32_t sf_id) {
+  return idesc_nvf4(m, n) | (1u << 23) | (sf_id << 4) | (sf_id << 29);
 }
 
 // Instruction descriptor of the MXFP8 block-scaled MMA: E4M3 x E4M3 -> fp32,

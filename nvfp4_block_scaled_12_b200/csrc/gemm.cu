@@ -5,7 +5,7 @@
 // next layer.
 //
 // One persistent kernel, templated on the tile shape (the same rule for the
-// NVFP4, fused, MXFP8 and row-wise FP8 GEMMs; gemm_config below):
+// NVFP4, fused, MXFP4, MXFP8 and row-wise FP8 GEMMs; gemm_config below):
 //   256 x 256 (wide)  a CTA pair (cluster of 2) owns the tile: each CTA loads
 //            its 128 rows of A and 128 rows of B, and the pair leader issues
 //            tcgen05.mma.cta_group::2 (M=256, N=256, K=64) into one
@@ -72,7 +72,9 @@ constexpr uint32_t kTmemCols = 512;
 // k-tile) against NVFP4 weights that the transform warps dequantize to bf16
 // in shared memory (the stage holds this CTA's B codes and scale atoms as
 // loaded, and the bf16 B tile the MMA reads).
-template <int kCG, int kBN, int kAcc, bool kMx, bool kRow = false, bool kW16 = false>
+// kMx4: MXFP4, E2M1 operands as NVFP4's with one E8M0 scale per 32 elements:
+// half the scale atoms to load and to move into TMEM.
+template <int kCG, int kBN, int kAcc, bool kMx, bool kRow = false, bool kW16 = false, bool kMx4 = false>
 struct Cfg {
   // Wide tiles (256 columns, one accumulator): the accumulator is drained into
   // the registers of eight epilogue warps, so the next tile's MMAs can start
@@ -85,8 +87,9 @@ struct Cfg {
   // 512-byte scale atoms (128 rows x 4 scale columns) per 128-row block and
   // k-tile: NVFP4's k-tile is 4 MMA k-blocks of 64 elements with one 4-scale
   // word per row each; MXFP8's is 4 k-blocks of 32 whose scales share one word.
-  // (W4A16: a k-tile of 64 elements is one atom, read for B only)
-  static constexpr int kAtoms = (kMx || kW16) ? 1 : 4;
+  // (W4A16: a k-tile of 64 elements is one atom, read for B only.  MXFP4: 4
+  // k-blocks of 64 with two scales per row each, two k-blocks to a word)
+  static constexpr int kAtoms = (kMx || kW16) ? 1 : (kMx4 ? 2 : 4);
   static constexpr uint32_t kSfaBytes = (kRow || kW16) ? 0 : kAtoms * 512;
   static constexpr int kBNc = kBN / kCG;  // B rows per CTA
   static constexpr uint32_t kBBytes = kBNc * kBKBytes;
@@ -110,8 +113,10 @@ struct Cfg {
   // j - kSfSlots has arrived on that k-tile's empty barrier, which can only
   // be the phase they wait for while kSfSlots <= kStages.
   static constexpr uint32_t kSfbGroups = kBN / 32;       // 32-row groups of B scales per k-block
-  static constexpr uint32_t kSfaSlotCols = kMx ? 4 : 16;
-  static constexpr uint32_t kSfbSlotCols = kMx ? (kSfbGroups + 7) / 8 * 8 : 4 * kSfbGroups;
+  static constexpr uint32_t kSfaSlotCols = kMx ? 4 : (kMx4 ? 8 : 16);
+  static constexpr uint32_t kSfbSlotCols = kMx    ? (kSfbGroups + 7) / 8 * 8
+                                           : kMx4 ? (2 * kSfbGroups + 7) / 8 * 8
+                                                  : 4 * kSfbGroups;
   static constexpr int kSfSlotsFit = (kTmemCols - kAcc * kBN) / (kSfaSlotCols + kSfbSlotCols);
   static constexpr int kSfSlots = kSfSlotsFit < kStages ? (kSfSlotsFit > 8 ? 8 : kSfSlotsFit) : kStages;
   static constexpr uint32_t kSfaCol = kAcc * kBN;
@@ -139,6 +144,7 @@ struct Cfg {
   static_assert(!kWide || kCG == 2, "wide tiles are CTA pairs");
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   static_assert(!kW16 || (!kMx && !kRow), "W4A16 has bf16 activations and NVFP4 weights");
+  static_assert(!kMx4 || (!kMx && !kRow && !kW16), "MXFP4 is a format of its own");
   // K split: a CTA's fp32 partial tile, 128 rows of kBN + 4 floats (the pad
   // spreads the rows over the banks), in the idle stage ring
   static constexpr uint32_t kPartStride = (kBN + 4) * 4;
@@ -179,14 +185,14 @@ __device__ __forceinline__ void store_chunk_bf16(const CUtensorMap* tmap, uint8_
   }
 }
 
-template <int kCG, int kBN, int kAcc, bool kFused, bool kMx, bool kRow, bool kW16 = false>
-__global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16>::kThreads, 1)
+template <int kCG, int kBN, int kAcc, bool kFused, bool kMx, bool kRow, bool kW16 = false, bool kMx4 = false>
+__global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16, kMx4>::kThreads, 1)
     gemm_nvf4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                      const __grid_constant__ CUtensorMap tmap_sfa, const __grid_constant__ CUtensorMap tmap_sfb,
                      const __grid_constant__ CUtensorMap tmap_y, const __grid_constant__ GemmParams p) {
-  using C = Cfg<kCG, kBN, kAcc, kMx, kRow, kW16>;
+  using C = Cfg<kCG, kBN, kAcc, kMx, kRow, kW16, kMx4>;
   static_assert(!(kFused && kW16), "the fused quantize epilogue follows an NVFP4 GEMM");
-  static_assert(!(kFused && kMx), "the fused quantize epilogue writes NVFP4 after an NVFP4 GEMM");
+  static_assert(!(kFused && (kMx || kMx4)), "the fused quantize epilogue writes NVFP4 after an NVFP4 GEMM");
   static_assert(!kRow || kMx, "row-wise FP8 uses the 8-bit operand layout");
   constexpr int S = C::kStages;
   constexpr int R = C::kSfSlots;
@@ -355,8 +361,8 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16>::kThreads
   auto run_mma = [&]() {
     // ------------------------------------------------------------ MMA issuer (group leader)
     if (lane == 0 && leader) {
-      // one MMA k-block: NVFP4 reads 4 scale columns per k-block; MXFP8 reads
-      // byte kb of the k-tile's scale words (named in the descriptor and in
+      // one MMA k-block: NVFP4 reads 4 scale columns per k-block, MXFP4 two
+      // bytes of 4 columns per two k-blocks; MXFP8 reads byte kb of the k-tile's scale words (named in the descriptor and in
       // the top two bits of the scale addresses)
       auto mma = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t sfa, uint32_t sfb, int kb, uint32_t accum) {
         if constexpr (kW16) {
@@ -378,6 +384,16 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16>::kThreads
             tc_mma_mxf8_pair(d, ad, bd, idesc, sfa | sel, sfb | sel, accum);
           else
             tc_mma_mxf8(d, ad, bd, idesc, sfa | sel, sfb | sel, accum);
+        } else if constexpr (kMx4) {
+          // two k-blocks share a scale word: bytes 0-1, then bytes 2-3
+          const uint32_t id = static_cast<uint32_t>(kb & 1) * 2u;
+          const uint32_t idesc = idesc_mxf4(128 * kCG, kBN, id);
+          const uint32_t sa = (sfa + static_cast<uint32_t>(kb >> 1) * 4u) | (id << 30);
+          const uint32_t sb = (sfb + static_cast<uint32_t>(kb >> 1) * C::kSfbGroups) | (id << 30);
+          if (kCG == 2)
+            tc_mma_mxf4_pair(d, ad, bd, idesc, sa, sb, accum);
+          else
+            tc_mma_mxf4(d, ad, bd, idesc, sa, sb, accum);
         } else {
           constexpr uint32_t idesc = idesc_nvf4(128 * kCG, kBN);
           if (kCG == 2)
@@ -523,10 +539,12 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16>::kThreads
             tmem_st_32x32b_x8(t_quarter + C::kSfbCol + static_cast<uint32_t>(slot) * C::kSfbSlotCols + c * 8,
                               sb + 8 * c);
         } else {
-          uint32_t sa[16];
-          uint32_t sb[4 * C::kSfbGroups];
+          uint32_t sa[4 * C::kAtoms];
+          uint32_t sb[C::kSfbSlotCols];
 #pragma unroll
-          for (int kb = 0; kb < 4; ++kb) {
+          for (int g = C::kAtoms * C::kSfbGroups; g < static_cast<int>(C::kSfbSlotCols); ++g) sb[g] = 0u;
+#pragma unroll
+          for (int kb = 0; kb < C::kAtoms; ++kb) {
             const uint4 v = *reinterpret_cast<const uint4*>(ssfa + kb * 512);
             sa[4 * kb + 0] = v.x;
             sa[4 * kb + 1] = v.y;
@@ -535,7 +553,7 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16>::kThreads
             uint32_t w[4 * C::kSfbBlocks];
 #pragma unroll
             for (int blk = 0; blk < C::kSfbBlocks; ++blk) {
-              const uint4 u = *reinterpret_cast<const uint4*>(ssfb + blk * 4 * 512 + kb * 512);
+              const uint4 u = *reinterpret_cast<const uint4*>(ssfb + (blk * C::kAtoms + kb) * 512);
               w[4 * blk + 0] = u.x;
               w[4 * blk + 1] = u.y;
               w[4 * blk + 2] = u.z;
@@ -553,7 +571,10 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16>::kThreads
             fault = kFaultMmaWait;
             break;
           }
-          tmem_st_32x32b_x16(t_quarter + C::kSfaCol + static_cast<uint32_t>(slot) * C::kSfaSlotCols, sa);
+          if constexpr (kMx4)
+            tmem_st_32x32b_x8(t_quarter + C::kSfaCol + static_cast<uint32_t>(slot) * C::kSfaSlotCols, sa);
+          else if constexpr (!kW16)
+            tmem_st_32x32b_x16(t_quarter + C::kSfaCol + static_cast<uint32_t>(slot) * C::kSfaSlotCols, sa);
 #pragma unroll
           for (int c = 0; c < static_cast<int>(C::kSfbSlotCols / 8); ++c)
             tmem_st_32x32b_x8(t_quarter + C::kSfbCol + static_cast<uint32_t>(slot) * C::kSfbSlotCols + c * 8,
@@ -1007,10 +1028,10 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16>::kThreads
   }
 }
 
-template <int kCG, int kBN, int kAcc, bool kFused, bool kMx, bool kRow = false, bool kW16 = false>
+template <int kCG, int kBN, int kAcc, bool kFused, bool kMx, bool kRow = false, bool kW16 = false, bool kMx4 = false>
 cudaError_t launch(const GemmTensorMaps& m, const GemmParams& p, cudaStream_t stream, const DeviceInfo& dev) {
-  using C = Cfg<kCG, kBN, kAcc, kMx, kRow, kW16>;
-  auto kernel = gemm_nvf4_kernel<kCG, kBN, kAcc, kFused, kMx, kRow, kW16>;
+  using C = Cfg<kCG, kBN, kAcc, kMx, kRow, kW16, kMx4>;
+  auto kernel = gemm_nvf4_kernel<kCG, kBN, kAcc, kFused, kMx, kRow, kW16, kMx4>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
@@ -1117,6 +1138,19 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int num_kt, int num_sms) {
     }
   }
   return best;
+}
+
+cudaError_t launch_gemm_mxfp4(const GemmTensorMaps& m, const GemmParams& p, const GemmConfig& c, cudaStream_t stream,
+                              const DeviceInfo& dev) {
+  if (c.cta_group == 2 && c.tile_n == 256 && c.acc_bufs == 1)
+    return launch<2, 256, 1, false, false, false, false, true>(m, p, stream, dev);
+  if (c.cta_group == 2 && c.tile_n == 192 && c.acc_bufs == 2)
+    return launch<2, 192, 2, false, false, false, false, true>(m, p, stream, dev);
+  if (c.cta_group == 2 && c.tile_n == 128 && c.acc_bufs == 2)
+    return launch<2, 128, 2, false, false, false, false, true>(m, p, stream, dev);
+  if (c.cta_group == 1 && c.tile_n == 192 && c.acc_bufs == 2)
+    return launch<1, 192, 2, false, false, false, false, true>(m, p, stream, dev);
+  return cudaErrorInvalidConfiguration;
 }
 
 cudaError_t launch_gemm_w4a16(const GemmTensorMaps& m, const GemmParams& p, const GemmConfig& c, cudaStream_t stream,

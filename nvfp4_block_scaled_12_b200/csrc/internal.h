@@ -30,7 +30,7 @@ struct GemmParams {
   int32_t M, N, K;
   int32_t tiles_m, tiles_n, num_tiles;  // tiles_m counts (128 * CTA-group)-row tiles
   int32_t num_kt;  // k-tiles of 256 elements (last one may be partial)
-  int32_t kblocks; // MMA k-blocks in total: K / 64 (NVFP4) or K / 32 (MXFP8)
+  int32_t kblocks; // MMA k-blocks in total: K / 64 (NVFP4, MXFP4) or K / 32 (MXFP8)
   float alpha;
   float alpha_mul;            // the epilogue uses fl(alpha * alpha_mul) (1 when alpha is given whole)
   const float* alpha_scale;   // nullable: if set, the epilogue uses fl(alpha * alpha_scale[0]) instead
@@ -87,6 +87,9 @@ cudaError_t launch_quantize(const CUtensorMap& tmap_x, int tile_rows, int64_t M,
 // MXFP8 (E4M3 codes [M, K], E8M0 scales, one per 32 elements, swizzled).
 cudaError_t launch_quantize_mxfp8(const CUtensorMap& tmap_x, int tile_rows, int64_t M, int64_t K, uint8_t* codes,
                                   uint8_t* sf, cudaStream_t stream, const DeviceInfo& dev);
+// MXFP4 (E2M1 codes [M, K/2], E8M0 scales as MXFP8's).
+cudaError_t launch_quantize_mxfp4(const CUtensorMap& tmap_x, int tile_rows, int64_t M, int64_t K, uint8_t* codes,
+                                  uint8_t* sf, cudaStream_t stream, const DeviceInfo& dev);
 // Same, with g derived on the device from amax_in[0] (as the dynamic
 // variant derives it from its own amax pass); scale_out gets [amax, g].
 cudaError_t launch_quantize_from_amax(const CUtensorMap& tmap_x, int tile_rows, int64_t M, int64_t K,
@@ -106,10 +109,10 @@ struct GemmConfig {
   int acc_bufs;   // accumulator buffers in TMEM
 };
 GemmConfig gemm_config(int64_t M, int64_t N, int num_sms);
-// Tile shape and K split of a GEMM whose epilogue is the plain one (NVFP4 and
-// W4A16 with bias): when the tiles cannot fill the SMs, up to 8 CTAs (4 CTA
+// Tile shape and K split of a GEMM whose epilogue is the plain one (NVFP4,
+// MXFP4 and W4A16 with bias): when the tiles cannot fill the SMs, up to 8 CTAs (4 CTA
 // pairs) of a cluster share one tile over disjoint k-tile ranges.  num_kt:
-// k-tiles of the problem (256 elements for NVFP4, 64 for W4A16).
+// k-tiles of the problem (256 elements for NVFP4 and MXFP4, 64 for W4A16).
 struct GemmPlan {
   GemmConfig c;
   int k_split;
@@ -119,6 +122,9 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int num_kt, int num_sms);
 // row: row-wise FP8 (8-bit operands without block scales; requires mx).
 cudaError_t launch_gemm(const GemmTensorMaps& m, const GemmParams& p, const GemmConfig& c, bool fused, bool mx,
                         cudaStream_t stream, const DeviceInfo& dev, bool row = false);
+// MXFP4 operands (E2M1 codes [rows, K/2], E8M0 scales per 32 elements).
+cudaError_t launch_gemm_mxfp4(const GemmTensorMaps& m, const GemmParams& p, const GemmConfig& c, cudaStream_t stream,
+                              const DeviceInfo& dev);
 // W4A16: bf16 activations [M, K] x NVFP4 weights [N, K] dequantized in shared
 // memory (p.w_scale is the weight's per-tensor scale; p.alpha = 1);
 // maps: a = bf16 activations (64-element boxes), b = weight codes (32-byte

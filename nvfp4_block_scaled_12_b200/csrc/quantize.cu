@@ -55,12 +55,16 @@ struct QCfg {
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
-template <bool kDynamic, bool kMx, int kRows>
+// Output format of a quantize launch.
+enum class QFormat { kNvfp4, kMxfp8, kMxfp4 };
+
+template <bool kDynamic, QFormat kFormat, int kRows>
 __global__ void __launch_bounds__(QCfg<kRows>::kThreads, 1)
     quantize_kernel(const __grid_constant__ CUtensorMap tmap_x, int64_t M, int64_t K, float g,
                     uint8_t* __restrict__ codes, uint8_t* __restrict__ sf, int64_t tiles_k, int64_t n_tiles,
                     unsigned* fault_word, DynamicScaleArgs dyn) {
   using Q = QCfg<kRows>;
+  constexpr bool kMx = kFormat != QFormat::kNvfp4;  // power-of-two scales, one per 32 elements
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Q::kOffBar);
@@ -153,7 +157,7 @@ __global__ void __launch_bounds__(QCfg<kRows>::kThreads, 1)
     // 32-byte aligned codes rows (the usual case: every row starts at a
     // multiple of 32 bytes when the buffer does) take one 32-byte store
     const bool codes32 = (reinterpret_cast<uintptr_t>(codes) & 31u) == 0;
-    const int64_t mx_katoms = (K / 32 + 3) / 4;  // MXFP8 scale atoms per 128-row block
+    const int64_t mx_katoms = (K / 32 + 3) / 4;  // MXFP8 and MXFP4 scale atoms per 128-row block
 
     // Dynamic variant, once per consumer warp (every one of the 16 reaches
     // it exactly once, so the named barriers below always complete): fold
@@ -239,10 +243,12 @@ __global__ void __launch_bounds__(QCfg<kRows>::kThreads, 1)
       const int64_t row = (tile / tiles_k) * Q::kTileRows + rloc;
       const int64_t katom = tile % tiles_k;  // 64-column group of the tile
       if constexpr (kMx) {
-        // MXFP8: two 32-element blocks -> 64 E4M3 bytes and two E8M0 scale
-        // bytes (scale columns 2*katom, 2*katom + 1: half of a 4-byte word)
+        // two 32-element blocks -> 64 E4M3 bytes (MXFP8) or 64 E2M1 codes in
+        // 32 bytes (MXFP4) and two E8M0 scale bytes (scale columns 2*katom,
+        // 2*katom + 1: half of a 4-byte word)
+        constexpr int kWords = kFormat == QFormat::kMxfp8 ? 8 : 4;  // code words of a block
         uint32_t sfh = 0u;
-        uint32_t cw[16];
+        uint32_t cw[2 * kWords];
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
           float f[32];
@@ -258,19 +264,23 @@ __global__ void __launch_bounds__(QCfg<kRows>::kThreads, 1)
             f[8 * c + 6] = bf16_lo(u.w);
             f[8 * c + 7] = bf16_hi(u.w);
           }
-          uint32_t w[8];
-          sfh |= quantize_mx_block32(f, w) << (8 * blk);
+          uint32_t w[kWords];
+          if constexpr (kFormat == QFormat::kMxfp8)
+            sfh |= quantize_mx_block32(f, w) << (8 * blk);
+          else
+            sfh |= quantize_mxfp4_block32(f, w) << (8 * blk);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) cw[8 * blk + i] = w[i];
+          for (int i = 0; i < kWords; ++i) cw[kWords * blk + i] = w[i];
         }
         if (row < M) {
-          uint8_t* crow = codes + row * K + katom * 64;
+          uint8_t* crow = codes + (row * tiles_k + katom) * (8 * kWords);  // K == 64 * tiles_k
           if (codes32) {
-            st_global_v8(crow, *reinterpret_cast<const uint32_t(*)[8]>(cw));
-            st_global_v8(crow + 32, *reinterpret_cast<const uint32_t(*)[8]>(cw + 8));
+#pragma unroll
+            for (int c = 0; c < kWords / 4; ++c)
+              st_global_v8(crow + 32 * c, *reinterpret_cast<const uint32_t(*)[8]>(cw + 8 * c));
           } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < kWords / 2; ++c)
               *reinterpret_cast<uint4*>(crow + 16 * c) = make_uint4(cw[4 * c], cw[4 * c + 1], cw[4 * c + 2], cw[4 * c + 3]);
           }
         }
@@ -365,7 +375,7 @@ int quantize_tile_rows(int64_t M, int64_t K, int num_sms) {
 
 namespace {
 
-template <bool kDynamic, bool kMx, int kRows>
+template <bool kDynamic, QFormat kFormat, int kRows>
 cudaError_t launch_q(const CUtensorMap& tmap_x, const void* x, int64_t M, int64_t K, float g, uint8_t* codes,
                      uint8_t* sf, float* scale_out, uint32_t* scratch, const GridWaitSettings& wait,
                      cudaStream_t stream, const DeviceInfo& dev) {
@@ -374,7 +384,7 @@ cudaError_t launch_q(const CUtensorMap& tmap_x, const void* x, int64_t M, int64_
   const int64_t tiles_k = (K + Q::kCols - 1) / Q::kCols;
   const int64_t n_tiles = tiles_m * tiles_k;
   const int grid = static_cast<int>(n_tiles < dev.num_sms ? n_tiles : dev.num_sms);
-  auto kernel = quantize_kernel<kDynamic, kMx, kRows>;
+  auto kernel = quantize_kernel<kDynamic, kFormat, kRows>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::kSmemBytes);
   if (err != cudaSuccess) return err;
   if (!kDynamic) {
@@ -411,7 +421,7 @@ cudaError_t launch_q_amax(const CUtensorMap& tmap_x, int64_t M, int64_t K, uint8
   const int64_t tiles_k = (K + Q::kCols - 1) / Q::kCols;
   const int64_t n_tiles = tiles_m * tiles_k;
   const int grid = static_cast<int>(n_tiles < dev.num_sms ? n_tiles : dev.num_sms);
-  auto kernel = quantize_kernel<false, false, kRows>;
+  auto kernel = quantize_kernel<false, QFormat::kNvfp4, kRows>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::kSmemBytes);
   if (err != cudaSuccess) return err;
   kernel<<<grid, Q::kThreads, Q::kSmemBytes, stream>>>(tmap_x, M, K, 0.0f, codes, sf, tiles_k, n_tiles, dev.fault, dyn);
@@ -423,15 +433,22 @@ cudaError_t launch_q_amax(const CUtensorMap& tmap_x, int64_t M, int64_t K, uint8
 cudaError_t launch_quantize(const CUtensorMap& tmap_x, int tile_rows, int64_t M, int64_t K, float g, uint8_t* codes,
                             uint8_t* sf, cudaStream_t stream, const DeviceInfo& dev) {
   const GridWaitSettings none;
-  return tile_rows == 256 ? launch_q<false, false, 256>(tmap_x, nullptr, M, K, g, codes, sf, nullptr, nullptr, none, stream, dev)
-                          : launch_q<false, false, 128>(tmap_x, nullptr, M, K, g, codes, sf, nullptr, nullptr, none, stream, dev);
+  return tile_rows == 256 ? launch_q<false, QFormat::kNvfp4, 256>(tmap_x, nullptr, M, K, g, codes, sf, nullptr, nullptr, none, stream, dev)
+                          : launch_q<false, QFormat::kNvfp4, 128>(tmap_x, nullptr, M, K, g, codes, sf, nullptr, nullptr, none, stream, dev);
 }
 
 cudaError_t launch_quantize_mxfp8(const CUtensorMap& tmap_x, int tile_rows, int64_t M, int64_t K, uint8_t* codes,
                                   uint8_t* sf, cudaStream_t stream, const DeviceInfo& dev) {
   const GridWaitSettings none;
-  return tile_rows == 256 ? launch_q<false, true, 256>(tmap_x, nullptr, M, K, 0.0f, codes, sf, nullptr, nullptr, none, stream, dev)
-                          : launch_q<false, true, 128>(tmap_x, nullptr, M, K, 0.0f, codes, sf, nullptr, nullptr, none, stream, dev);
+  return tile_rows == 256 ? launch_q<false, QFormat::kMxfp8, 256>(tmap_x, nullptr, M, K, 0.0f, codes, sf, nullptr, nullptr, none, stream, dev)
+                          : launch_q<false, QFormat::kMxfp8, 128>(tmap_x, nullptr, M, K, 0.0f, codes, sf, nullptr, nullptr, none, stream, dev);
+}
+
+cudaError_t launch_quantize_mxfp4(const CUtensorMap& tmap_x, int tile_rows, int64_t M, int64_t K, uint8_t* codes,
+                                  uint8_t* sf, cudaStream_t stream, const DeviceInfo& dev) {
+  const GridWaitSettings none;
+  return tile_rows == 256 ? launch_q<false, QFormat::kMxfp4, 256>(tmap_x, nullptr, M, K, 0.0f, codes, sf, nullptr, nullptr, none, stream, dev)
+                          : launch_q<false, QFormat::kMxfp4, 128>(tmap_x, nullptr, M, K, 0.0f, codes, sf, nullptr, nullptr, none, stream, dev);
 }
 
 cudaError_t launch_quantize_from_amax(const CUtensorMap& tmap_x, int tile_rows, int64_t M, int64_t K,
@@ -448,8 +465,8 @@ cudaError_t launch_quantize_dynamic(const CUtensorMap& tmap_x, int tile_rows, co
                                     uint8_t* codes, uint8_t* sf, float* scale_out, uint32_t* scratch,
                                     const GridWaitSettings& wait, cudaStream_t stream, const DeviceInfo& dev) {
   return tile_rows == 256
-             ? launch_q<true, false, 256>(tmap_x, x, M, K, 0.0f, codes, sf, scale_out, scratch, wait, stream, dev)
-             : launch_q<true, false, 128>(tmap_x, x, M, K, 0.0f, codes, sf, scale_out, scratch, wait, stream, dev);
+             ? launch_q<true, QFormat::kNvfp4, 256>(tmap_x, x, M, K, 0.0f, codes, sf, scale_out, scratch, wait, stream, dev)
+             : launch_q<true, QFormat::kNvfp4, 128>(tmap_x, x, M, K, 0.0f, codes, sf, scale_out, scratch, wait, stream, dev);
 }
 
 cudaError_t launch_swizzle_sf(const uint8_t* sf_lin, int64_t rows, int64_t k, uint8_t* out,

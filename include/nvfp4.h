@@ -435,6 +435,64 @@ nvfp4_status nvfp4_mxfp4_gemm(const uint8_t* a, const uint8_t* sfa, const uint8_
 
 /*
  * ------------------------------------------------------------------------
+ * Between the linear layers of an attention block: rotary positions and
+ * attention on 16-bit heads, as the GEMMs' epilogues write them.
+ * ------------------------------------------------------------------------
+ */
+enum { NVFP4_DTYPE_BF16 = 0, NVFP4_DTYPE_FP16 = 1 };
+
+/* A [batch, tokens, heads, head_dim] tensor of 16-bit elements: strides in
+ * elements, multiples of 8 (those of extents of one are not read), head_dim
+ * contiguous, data 16-byte aligned.  The Q, K or V columns of a fused
+ * projection [tokens, ld] are head_stride = head_dim, token_stride = ld. */
+typedef struct {
+  void* data;
+  int64_t batch_stride, token_stride, head_stride;
+} nvfp4_heads;
+
+#define NVFP4_ROPE_MAX_AXES 4
+enum { NVFP4_POS_INT32 = 0, NVFP4_POS_FLOAT32 = 1 };
+enum { NVFP4_ROPE_INTERLEAVED = 1, NVFP4_ROPE_SHARED_LADDER = 2 };
+
+/* One tensor to rotate.  out may be in itself (in place), or must not overlap
+ * it.  norm_weight [head_dim] (of the tensor's type) or NULL: with it, each
+ * head is first divided by its root mean square and multiplied by the weight. */
+typedef struct {
+  nvfp4_heads in, out;
+  int64_t heads;
+  const void* norm_weight;
+} nvfp4_rope_tensor;
+
+/*
+ * Rotary positions with up to NVFP4_ROPE_MAX_AXES axes, one launch for up to
+ * two tensors (Q and K) of the same batch, tokens and head width.  Of every
+ * head x the first R = sum(axis_dims) elements turn in R/2 pairs; pair i with
+ * elements (a, b) on axis j, the i_j-th pair of that axis:
+ *     phi = pos[batch, token, j] * theta^(-2 i_j / axis_dims[j])
+ *           (NVFP4_ROPE_SHARED_LADDER: pos * theta^(-2 i / R))
+ *     (a, b) <- (a cos phi - b sin phi, a sin phi + b cos phi)
+ * Pairs are (2i, 2i+1) with NVFP4_ROPE_INTERLEAVED, else (i, i + R/2); the
+ * elements from R on pass through.  With a norm_weight, x is first
+ * x / sqrt(mean(x^2) + eps) * weight over the whole head.  Angles are reduced
+ * in 64 bits, the rest is fp32, rounded once.
+ *   dtype      NVFP4_DTYPE_BF16 or _FP16, of all tensors and weights
+ *   positions  [tokens, n_axes] int32 or fp32 (pos_type), row-major, of every
+ *              batch entry (pos_batch_stride = 0) or pos_batch_stride elements
+ *              apart; 4-byte aligned
+ *   axis_dims  host array of n_axes even widths; their sum R is a multiple of
+ *              8 and at most head_dim
+ * batch, tokens, heads >= 1; head_dim a multiple of 8, at most 256; theta > 0;
+ * eps >= 0.  Errors: EINVAL, EALIGN, EARCH, ECUDA.
+ */
+nvfp4_status nvfp4_rope(const nvfp4_rope_tensor* tensors, int32_t n_tensors,
+                        int64_t batch, int64_t tokens, int64_t head_dim,
+                        int32_t dtype, const void* positions, int32_t pos_type,
+                        int64_t pos_batch_stride, int32_t n_axes,
+                        const int32_t* axis_dims, double theta, int32_t flags,
+                        float eps, void* stream);
+
+/*
+ * ------------------------------------------------------------------------
  * Row-wise FP8 (W8A8) variant (BFL doc, `fp8r` bullet and "Kernels" row
  * `fp8r`: an E4M3 `weight` with one fp32 `weight_scale` per row;
  * activations quantized to E4M3 row by row at run time; the GEMM applies the

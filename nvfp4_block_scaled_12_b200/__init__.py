@@ -25,6 +25,9 @@ LIB_PATH = os.path.join(_HERE, "libnvfp4.so")
 
 NVFP4_OK, NVFP4_EINVAL, NVFP4_EALIGN, NVFP4_EARCH, NVFP4_ECUDA, NVFP4_ETIMEOUT = range(6)
 ACT_NONE, ACT_GELU_TANH = 0, 1
+DTYPE_BF16, DTYPE_FP16 = 0, 1
+POS_INT32, POS_FLOAT32 = 0, 1
+ROPE_INTERLEAVED, ROPE_SHARED_LADDER = 1, 2
 DST_BF16, DST_NVFP4 = 0, 1
 MAX_RANGES = 8
 NVFP4_DYNAMIC_WORKSPACE_BYTES = 8
@@ -44,6 +47,17 @@ class ColRange(ctypes.Structure):
     """``nvfp4_colrange``: one column range of the fused epilogue."""
     _fields_ = [("begin", ctypes.c_int64), ("end", ctypes.c_int64), ("act", ctypes.c_int32),
                 ("dst", ctypes.c_int32), ("dst_col", ctypes.c_int64)]
+
+
+class Heads(ctypes.Structure):
+    """``nvfp4_heads``: a [batch, tokens, heads, head_dim] tensor, strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class RopeTensor(ctypes.Structure):
+    """``nvfp4_rope_tensor``: one tensor that ``nvfp4_rope`` rotates."""
+    _fields_ = [("in_", Heads), ("out", Heads), ("heads", ctypes.c_int64), ("norm_weight", ctypes.c_void_p)]
 
 
 def _load() -> ctypes.CDLL:
@@ -78,6 +92,8 @@ def _load() -> ctypes.CDLL:
     lib.nvfp4_mxfp4_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, f32, vp, vp, vp]
     lib.nvfp4_fp8row_quantize.argtypes = [vp, i64, i64, vp, vp, vp]
     lib.nvfp4_fp8row_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp, vp]
+    lib.nvfp4_rope.argtypes = [ctypes.POINTER(RopeTensor), i32, i64, i64, i64, i32, vp, i32, i64, i32,
+                               ctypes.POINTER(ctypes.c_int32), ctypes.c_double, i32, f32, vp]
     lib.nvfp4_dequantize.argtypes = [vp, vp, f32, i64, i64, vp, vp]
     lib.nvfp4_w4a16_gemm.argtypes = [vp, vp, vp, i64, i64, i64, f32, vp, vp, vp]
     lib.nvfp4_check_fault.argtypes = []
@@ -91,7 +107,7 @@ def _load() -> ctypes.CDLL:
                  "nvfp4_dequantize", "nvfp4_check_fault", "nvfp4_gemm_tile_shape", "nvfp4_gemm_scaled",
                  "nvfp4_gemm_quant_scaled", "nvfp4_testing_set_grid_wait", "nvfp4_w4a16_gemm",
                  "nvfp4_gemm_plan", "nvfp4_gemm_amax", "nvfp4_quantize_from_amax", "nvfp4_mxfp4_quantize",
-                 "nvfp4_mxfp4_gemm"):
+                 "nvfp4_mxfp4_gemm", "nvfp4_rope"):
         getattr(lib, name).restype = ctypes.c_int
     lib.nvfp4_last_error.argtypes = []
     lib.nvfp4_last_error.restype = ctypes.c_char_p
@@ -223,6 +239,15 @@ def nvfp4_fp8row_quantize(x: int, M: int, K: int, codes: int, scale: int, stream
 def nvfp4_fp8row_gemm(a: int, a_scale: int, b: int, b_scale: int, M: int, N: int, K: int, bias: int, y: int,
                       stream: int) -> None:
     _check(library().nvfp4_fp8row_gemm(a, a_scale, b, b_scale, M, N, K, bias or None, y, stream))
+
+
+def nvfp4_rope(tensors: Sequence[RopeTensor], batch: int, tokens: int, head_dim: int, dtype: int, positions: int,
+               pos_type: int, pos_batch_stride: int, axis_dims: Sequence[int], theta: float, flags: int, eps: float,
+               stream: int) -> None:
+    arr = (RopeTensor * len(tensors))(*tensors)
+    dims = (ctypes.c_int32 * len(axis_dims))(*axis_dims)
+    _check(library().nvfp4_rope(arr, len(tensors), batch, tokens, head_dim, dtype, positions, pos_type,
+                                pos_batch_stride, len(axis_dims), dims, theta, flags, eps, stream))
 
 
 def nvfp4_dequantize(codes: int, sf: int, g: float, rows: int, K: int, out: int, stream: int) -> None:
@@ -615,6 +640,85 @@ def linear_w4a16(x, w: NVFP4Tensor, bias=None, y=None, stream=None):
     _need(y, torch.bfloat16, (M, N), "y", dev=dev)
     nvfp4_w4a16_gemm(_ptr(x), _ptr(w.codes), _ptr(w.sf), M, N, K, float(w.g), _ptr(bias), _ptr(y), _stream(stream))
     return y
+
+
+def _need_heads(t, name, dtype=None, shape=None, dev=None):
+    """``t`` must be a bf16 or fp16 CUDA tensor [batch, tokens, heads,
+    head_dim] on the current device with contiguous heads; the library checks
+    the other strides, which may be any multiple of 8."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype if dtype is not None else t.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name} must be {dtype or 'bfloat16 or float16'}, got {t.dtype}")
+    if t.dim() != 4 or 0 in t.shape:
+        raise ValueError(f"{name} must be [batch, tokens, heads, head_dim], none of them 0, got {tuple(t.shape)}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}'s heads must be contiguous")
+    if t.device.index != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _heads(t) -> Heads:
+    sb, st, sh, _ = t.stride()
+    return Heads(t.data_ptr(), sb, st, sh)
+
+
+def _empty_on(stream, shape, like):
+    """A new tensor of ``like``'s type, owned by the stream that writes it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+
+
+def rope(q, positions, axes: Sequence[int], k=None, theta: float = 10000.0, q_weight=None, k_weight=None,
+         eps: float = 1e-6, interleaved: bool = True, shared: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary positions with several axes on bf16 or fp16 heads ``q`` (and
+    ``k``) [batch, tokens, heads, head_dim], in one launch.
+
+    ``positions`` is int32 or float32 [tokens, len(axes)] or [batch, tokens,
+    len(axes)]; ``axes`` gives the elements of each head that turn with each
+    axis (the rest of the head passes through).  Pairs are neighbours
+    (``interleaved``) or halves; each axis has its own ladder of frequencies
+    theta^(-2i/d), or all pairs one (``shared``).  With ``q_weight`` /
+    ``k_weight`` [head_dim] that tensor's heads are RMS-normed first.  Returns
+    the rotated q, or (q, k) when ``k`` is given; ``q_out`` / ``k_out`` take
+    the results (the inputs themselves, to work in place)."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    _need_heads(q, "q", dev=dev)
+    B, L, _, D = q.shape
+    if k is None and (k_weight is not None or k_out is not None):
+        raise ValueError("k_weight and k_out need k")
+    results, args = [], []
+    for name, x, weight, out in (("q", q, q_weight, q_out), ("k", k, k_weight, k_out)):
+        if x is None:
+            continue
+        if name == "k":
+            _need_heads(x, name, q.dtype, (B, L, x.shape[2] if x.dim() == 4 else 0, D), dev=dev)
+        if weight is not None:
+            _need(weight, q.dtype, (D,), f"{name}_weight", dev=dev)
+        if out is None:
+            out = _empty_on(stream, x.shape, x)
+        else:
+            _need_heads(out, f"{name}_out", q.dtype, x.shape, dev=dev)
+        results.append(out)
+        args.append(RopeTensor(_heads(x), _heads(out), x.shape[2], _ptr(weight)))
+    if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.float32):
+        raise TypeError("positions must be an int32 or float32 CUDA tensor")
+    n = len(axes)
+    if tuple(positions.shape) not in ((L, n), (B, L, n)):
+        raise ValueError(f"positions must be [{L}, {n}] or [{B}, {L}, {n}], got {tuple(positions.shape)}")
+    _need(positions, positions.dtype, None, "positions", dev=dev)
+    nvfp4_rope(args, B, L, D, DTYPE_FP16 if q.dtype == torch.float16 else DTYPE_BF16, _ptr(positions),
+               POS_FLOAT32 if positions.dtype == torch.float32 else POS_INT32, L * n if positions.dim() == 3 else 0,
+               axes, float(theta), ROPE_INTERLEAVED * bool(interleaved) + ROPE_SHARED_LADDER * bool(shared),
+               float(eps), _stream(stream))
+    return results[0] if k is None else tuple(results)
 
 
 def swizzle_sf(sf_linear, rows: int, k: int, stream=None):

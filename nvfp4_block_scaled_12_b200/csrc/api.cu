@@ -272,6 +272,25 @@ nvfp4_status gemm_common(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
   return make_sf_tmap(&maps->sfb, sfb, N, atoms, box_atoms, sfb_blocks, "B scales");
 }
 
+// Checks one heads tensor: extents are those of the call, strides those of
+// extents above one.  written: two elements may not share an address.
+nvfp4_status check_heads(const char* name, const nvfp4_heads& t, int64_t batch, int64_t tokens, int64_t heads,
+                         int64_t head_dim, bool written) {
+  if (!t.data) return fail(NVFP4_EINVAL, "%s: null pointer", name);
+  if (!aligned16(t.data)) return fail(NVFP4_EALIGN, "%s must be 16-byte aligned", name);
+  const int64_t extent[3] = {batch, tokens, heads};
+  const int64_t stride[3] = {t.batch_stride, t.token_stride, t.head_stride};
+  for (int i = 0; i < 3; ++i) {
+    if (extent[i] == 1) continue;
+    if (stride[i] < 0 || stride[i] % 8 != 0 || stride[i] > (int64_t(1) << 38))
+      return fail(NVFP4_EINVAL, "%s: stride %lld must be a multiple of 8 in [0, 2^38]", name, (long long)stride[i]);
+    if (written && stride[i] < head_dim)
+      return fail(NVFP4_EINVAL, "%s: stride %lld lets two heads of %lld overlap", name, (long long)stride[i],
+                  (long long)head_dim);
+  }
+  return NVFP4_OK;
+}
+
 // nvfp4_gemm_quant with alpha = fl(alpha * alpha_mul) formed on the device.
 nvfp4_status gemm_quant_impl(const uint8_t* a, const uint8_t* sfa, const uint8_t* b, const uint8_t* sfb,
                              int64_t M, int64_t N, int64_t K, float alpha, float alpha_mul, const void* bias,
@@ -434,6 +453,90 @@ nvfp4_status nvfp4_mxfp4_gemm(const uint8_t* a, const uint8_t* sfa, const uint8_
   if (st != NVFP4_OK) return st;
   cudaError_t e = launch_gemm_mxfp4(maps, p, cg, static_cast<cudaStream_t>(stream), *dev);
   if (e != cudaSuccess) return cuda_fail(e, "mxfp4 gemm launch");
+  return ok();
+}
+
+nvfp4_status nvfp4_rope(const nvfp4_rope_tensor* tensors, int32_t n_tensors, int64_t batch, int64_t tokens,
+                        int64_t head_dim, int32_t dtype, const void* positions, int32_t pos_type,
+                        int64_t pos_batch_stride, int32_t n_axes, const int32_t* axis_dims, double theta,
+                        int32_t flags, float eps, void* stream) {
+  if (!tensors || n_tensors < 1 || n_tensors > 2) return fail(NVFP4_EINVAL, "n_tensors=%d must be 1 or 2", n_tensors);
+  if (!positions || !axis_dims) return fail(NVFP4_EINVAL, "null pointer");
+  if (batch < 1 || tokens < 1 || batch > kMaxDim || tokens > kMaxDim || batch * tokens > kMaxDim)
+    return fail(NVFP4_EINVAL, "batch=%lld and tokens=%lld must be positive, their product at most %lld",
+                (long long)batch, (long long)tokens, (long long)kMaxDim);
+  if (head_dim < 8 || head_dim % 8 != 0 || head_dim > 2 * kRopeMaxPairs)
+    return fail(NVFP4_EINVAL, "head_dim=%lld must be a multiple of 8 in [8, %d]", (long long)head_dim,
+                2 * kRopeMaxPairs);
+  if (dtype != NVFP4_DTYPE_BF16 && dtype != NVFP4_DTYPE_FP16) return fail(NVFP4_EINVAL, "unknown dtype %d", dtype);
+  if (pos_type != NVFP4_POS_INT32 && pos_type != NVFP4_POS_FLOAT32)
+    return fail(NVFP4_EINVAL, "unknown pos_type %d", pos_type);
+  if (reinterpret_cast<uintptr_t>(positions) % 4 != 0) return fail(NVFP4_EALIGN, "positions must be 4-byte aligned");
+  if (pos_batch_stride < 0) return fail(NVFP4_EINVAL, "pos_batch_stride must not be negative");
+  if (n_axes < 1 || n_axes > kRopeMaxAxes)
+    return fail(NVFP4_EINVAL, "n_axes=%d must be in [1, %d]", n_axes, kRopeMaxAxes);
+  if (!(theta > 0.0) || !isfinite(theta)) return fail(NVFP4_EINVAL, "theta must be positive and finite");
+  if (flags & ~(NVFP4_ROPE_INTERLEAVED | NVFP4_ROPE_SHARED_LADDER)) return fail(NVFP4_EINVAL, "unknown flags");
+  if (!(eps >= 0.0f) || !finite_f(eps)) return fail(NVFP4_EINVAL, "eps must be finite and not negative");
+  int64_t rotated = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (axis_dims[a] < 2 || axis_dims[a] % 2 != 0 || axis_dims[a] > head_dim)
+      return fail(NVFP4_EINVAL, "axis_dims[%d]=%d must be even, in [2, head_dim]", a, axis_dims[a]);
+    rotated += axis_dims[a];
+  }
+  if (rotated > head_dim || rotated % 8 != 0)
+    return fail(NVFP4_EINVAL, "axis_dims add up to %lld: a multiple of 8, at most head_dim, needed",
+                (long long)rotated);
+  RopeParams p = {};
+  bool norm = false;
+  for (int i = 0; i < n_tensors; ++i) {
+    const nvfp4_rope_tensor& t = tensors[i];
+    if (t.heads < 1 || t.heads > 65535) return fail(NVFP4_EINVAL, "heads=%lld must be in [1, 65535]", (long long)t.heads);
+    nvfp4_status st = check_heads("in", t.in, batch, tokens, t.heads, head_dim, false);
+    if (st == NVFP4_OK) st = check_heads("out", t.out, batch, tokens, t.heads, head_dim, true);
+    if (st != NVFP4_OK) return st;
+    if (!aligned16(t.norm_weight)) return fail(NVFP4_EALIGN, "norm_weight must be 16-byte aligned");
+    // (a stride that is not read, of an extent of one, is passed on as 0)
+    p.t[i] = RopeTensor{t.in.data,
+                        t.out.data,
+                        batch > 1 ? t.in.batch_stride : 0,
+                        tokens > 1 ? t.in.token_stride : 0,
+                        t.heads > 1 ? t.in.head_stride : 0,
+                        batch > 1 ? t.out.batch_stride : 0,
+                        tokens > 1 ? t.out.token_stride : 0,
+                        t.heads > 1 ? t.out.head_stride : 0,
+                        t.norm_weight,
+                        static_cast<int32_t>(t.heads)};
+    norm |= t.norm_weight != nullptr;
+  }
+  p.positions = positions;
+  p.pos_batch_stride = pos_batch_stride;
+  p.L = static_cast<int32_t>(tokens);
+  p.D = static_cast<int32_t>(head_dim);
+  p.R = static_cast<int32_t>(rotated);
+  p.n_axes = n_axes;
+  p.pos_float = pos_type == NVFP4_POS_FLOAT32;
+  p.eps = eps;
+  // turns per position of every pair, theta^(-2i/d) / 2 pi: a geometric ladder
+  // per axis, or one over all pairs (its steps multiplied up in 64 bits)
+  const double per_turn = 0.15915494309189533576888;  // 1 / 2 pi
+  int pair = 0;
+  double f = per_turn;
+  for (int a = 0; a < n_axes; ++a) {
+    p.first_pair[a] = pair;
+    const bool shared = (flags & NVFP4_ROPE_SHARED_LADDER) != 0;
+    if (!shared) f = per_turn;
+    const double step = pow(theta, -2.0 / static_cast<double>(shared ? rotated : axis_dims[a]));
+    for (int i = 0; i < axis_dims[a] / 2; ++i, f *= step) p.turns[pair++] = f;
+  }
+  const DeviceInfo* dev = nullptr;
+  nvfp4_status st = current_device(&dev);
+  if (st != NVFP4_OK) return st;
+  int64_t blocks = 0;
+  if (!rope_plan(&p, batch * tokens, dev->num_sms, &blocks)) return fail(NVFP4_EINVAL, "problem too large");
+  cudaError_t e = launch_rope(p, blocks, dtype == NVFP4_DTYPE_FP16, (flags & NVFP4_ROPE_INTERLEAVED) != 0, norm,
+                              static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope launch");
   return ok();
 }
 

@@ -138,4 +138,31 @@ cudaError_t launch_dequantize(const uint8_t* codes, const uint8_t* sf, float g, 
 cudaError_t launch_quantize_rowwise(const void* x, int64_t M, int64_t K, uint8_t* codes, float* scale,
                                     cudaStream_t stream);
 
+// Rotary positions (csrc/rope.cu).  Strides in elements.
+constexpr int kRopeMaxAxes = NVFP4_ROPE_MAX_AXES;
+constexpr int kRopeMaxPairs = 128;  // head widths up to 256
+struct RopeTensor {
+  const void* in;
+  void* out;
+  int64_t in_batch, in_token, in_head, out_batch, out_token, out_head;
+  const void* weight;  // RMS norm weight [D], nullable
+  int32_t heads;
+};
+struct RopeParams {
+  RopeTensor t[2];  // the second one with heads == 0 when there is none
+  const void* positions;
+  int64_t pos_batch_stride;
+  int64_t units;  // groups of lanes at work, one per token and run of heads
+  int32_t L, D, R;
+  int32_t n_axes, first_pair[kRopeMaxAxes];
+  int32_t pos_float;
+  int32_t group, heads_per_unit, parts0, units_per_token;
+  float eps;
+  double turns[kRopeMaxPairs];  // a pair's turns per position: f / 2 pi
+};
+// Fills the launch shape for `tokens` = B * L; false when the grid is too large.
+bool rope_plan(RopeParams* p, int64_t tokens, int num_sms, int64_t* blocks);
+cudaError_t launch_rope(const RopeParams& p, int64_t blocks, bool fp16, bool interleaved, bool norm,
+                        cudaStream_t stream);
+
 }  // namespace nvfp4

@@ -1,0 +1,91 @@
+"""Argument checks of the entry points on 16-bit heads, on the CPU: the C ABI
+refuses before it touches a device, the torch helpers before they hand a
+pointer on."""
+import pytest
+import torch
+
+import nvfp4_block_scaled_12_b200 as F
+from tests.test_abi import P, _expect
+from tests.test_binding_checks import empty
+
+BF = torch.bfloat16
+
+
+def heads(batch=64 * 512, token=512, head=64, data=P):
+    return F.Heads(data, batch, token, head)
+
+
+def rope_args(**kw):
+    a = dict(tensors=[F.RopeTensor(heads(), heads(), 8, 0)], batch=2, tokens=64, head_dim=64, dtype=0, positions=P,
+             pos_type=0, pos_batch_stride=0, axis_dims=[16, 24, 24], theta=1e4, flags=1, eps=1e-6, stream=0)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(tensors=[]), dict(batch=0), dict(tokens=0), dict(batch=1 << 20, tokens=1 << 20), dict(head_dim=60),
+    dict(head_dim=264), dict(head_dim=0), dict(dtype=2), dict(positions=0), dict(pos_type=2),
+    dict(pos_batch_stride=-1), dict(axis_dims=[]), dict(axis_dims=[8] * 5), dict(axis_dims=[15, 25]),
+    dict(axis_dims=[64, 2]), dict(axis_dims=[10, 10]), dict(axis_dims=[0, 8]), dict(theta=0.0),
+    dict(theta=float("nan")), dict(theta=float("inf")), dict(flags=4), dict(eps=-1.0), dict(eps=float("nan")),
+    dict(tensors=[F.RopeTensor(heads(), heads(), 0, 0)]), dict(tensors=[F.RopeTensor(heads(), heads(), 1 << 20, 0)]),
+    dict(tensors=[F.RopeTensor(heads(data=0), heads(), 8, 0)]),
+    dict(tensors=[F.RopeTensor(heads(token=508), heads(), 8, 0)]),
+    dict(tensors=[F.RopeTensor(heads(token=-512), heads(), 8, 0)]),
+    dict(tensors=[F.RopeTensor(heads(), heads(head=56), 8, 0)]),
+    dict(tensors=[F.RopeTensor(heads(), heads(batch=0), 8, 0)]),
+    dict(tensors=[F.RopeTensor(heads(), heads(), 8, 0)] * 3)])
+def test_rope_rejects_bad_arguments(kw):
+    _expect(F.NVFP4_EINVAL, F.nvfp4_rope, *rope_args(**kw))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(positions=P + 2), dict(tensors=[F.RopeTensor(heads(data=P + 8), heads(), 8, 0)]),
+    dict(tensors=[F.RopeTensor(heads(), heads(data=P + 2), 8, 0)]),
+    dict(tensors=[F.RopeTensor(heads(), heads(), 8, P + 4)])])
+def test_rope_rejects_unaligned_pointers(kw):
+    _expect(F.NVFP4_EALIGN, F.nvfp4_rope, *rope_args(**kw))
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    rec = []
+    for name in ("nvfp4_rope",):
+        monkeypatch.setattr(F, name, lambda *a, _n=name: rec.append((_n, a)))
+    monkeypatch.setattr(F, "_stream", lambda stream: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    return rec
+
+
+def test_rope_helper(calls):
+    q, k = empty(2, 9, 4, 64, dtype=BF), empty(2, 9, 2, 64, dtype=BF)
+    qo, ko = empty(2, 9, 4, 64, dtype=BF), empty(2, 9, 2, 64, dtype=BF)
+    pos, w = empty(9, 2, dtype=torch.int32), empty(64, dtype=BF)
+    got = F.rope(q, pos, [32, 32], k=k, q_weight=w, q_out=qo, k_out=ko)
+    assert got[0] is qo and got[1] is ko
+    assert F.rope(q, empty(2, 9, 2, dtype=torch.float32), [32, 32], q_out=q) is q
+    (_, a), (_, b) = calls
+    assert len(a[0]) == 2 and a[0][0].norm_weight and not a[0][1].norm_weight and a[0][1].heads == 2
+    assert a[1:5] == (2, 9, 64, 0) and a[6] == F.POS_INT32 and a[7] == 0 and b[6] == F.POS_FLOAT32 and b[7] == 18
+    wide = empty(2, 9, 4, 128, dtype=BF)
+    for bad in (lambda: F.rope(empty(2, 9, 4, 64, dtype=torch.float32), pos, [32, 32], q_out=qo),
+                lambda: F.rope(q[0], pos, [32, 32], q_out=qo),
+                lambda: F.rope(wide[..., ::2], pos, [32, 32], q_out=qo),
+                lambda: F.rope(empty(2, 9, 4, 64, dtype=BF, dev=1), pos, [32, 32], q_out=qo),
+                lambda: F.rope(q, pos, [32, 32], q_out=ko),
+                lambda: F.rope(q, pos, [32, 32], q_out=empty(2, 9, 4, 64, dtype=torch.float16)),
+                lambda: F.rope(q, pos, [32, 32], k=empty(2, 8, 2, 64, dtype=BF), q_out=qo, k_out=ko),
+                lambda: F.rope(q, pos, [32, 32], k=empty(2, 9, 2, 72, dtype=BF), q_out=qo),
+                lambda: F.rope(q, pos, [32, 32], k=empty(2, 9, 2, 64, dtype=torch.float16), q_out=qo),
+                lambda: F.rope(q, pos, [32, 32], k_weight=w, q_out=qo),
+                lambda: F.rope(q, pos, [32, 32], q_weight=empty(32, dtype=BF), q_out=qo),
+                lambda: F.rope(q, pos, [32, 32], q_weight=empty(64, dtype=torch.float32), q_out=qo),
+                lambda: F.rope(q, pos, [64], q_out=qo),
+                lambda: F.rope(q, empty(8, 2, dtype=torch.int32), [32, 32], q_out=qo),
+                lambda: F.rope(q, empty(9, 2, dtype=torch.int64), [32, 32], q_out=qo),
+                lambda: F.rope(q, empty(9, 2, dtype=torch.int32, dev=1), [32, 32], q_out=qo),
+                lambda: F.rope(q, empty(2, 9, dtype=torch.int32).t(), [32, 32], q_out=qo),
+                lambda: F.rope(empty(2, 0, 4, 64, dtype=BF), empty(0, 2, dtype=torch.int32), [32, 32])):
+        with pytest.raises((TypeError, ValueError)):
+            bad()
+    assert len(calls) == 2

@@ -492,6 +492,33 @@ nvfp4_status nvfp4_rope(const nvfp4_rope_tensor* tensors, int32_t n_tensors,
                         float eps, void* stream);
 
 /*
+ * Attention of q_tokens queries over kv_tokens states of another sequence
+ * (or, for joint attention, of the same one), per batch entry and head:
+ *     out = softmax(scale * q k^T) v   over the states [0, kv_lens[b])
+ * Query head h reads K/V head h / (q_heads / kv_heads).  Scores, maxima, sums
+ * and the output's sum are fp32; the probabilities are rounded to the type
+ * for the product with v; the result is rounded once.
+ *   q, out     [batch, q_tokens, q_heads, head_dim]
+ *   k, v       [batch, kv_tokens, kv_heads, head_dim]; a batch_stride of 0
+ *              shares one entry with the whole batch (so may q's)
+ *   dtype      NVFP4_DTYPE_BF16 or _FP16, of all four
+ *   kv_lens    device array [batch] of valid states (clamped into
+ *              [0, kv_tokens]), read when the kernel runs, or NULL for all.
+ *              What k and v hold from there on does not matter, NaN included;
+ *              an entry without states gets zeros.
+ *   scale      positive and finite (1 / sqrt(head_dim) as a rule)
+ * Every extent >= 1; head_dim a multiple of 8, at most 128; q_heads a multiple
+ * of kv_heads, at most 128 of them to a K/V head; out overlaps no input.  The
+ * same inputs give the same bits.  Errors: EINVAL, EALIGN, EARCH, ECUDA; a
+ * barrier time-out records NVFP4_ETIMEOUT (nvfp4_check_fault).
+ */
+nvfp4_status nvfp4_attention(const nvfp4_heads* q, const nvfp4_heads* k, const nvfp4_heads* v,
+                             const nvfp4_heads* out, int64_t batch, int64_t q_tokens,
+                             int64_t kv_tokens, int64_t q_heads, int64_t kv_heads,
+                             int64_t head_dim, int32_t dtype, const int32_t* kv_lens,
+                             float scale, void* stream);
+
+/*
  * ------------------------------------------------------------------------
  * Row-wise FP8 (W8A8) variant (BFL doc, `fp8r` bullet and "Kernels" row
  * `fp8r`: an E4M3 `weight` with one fp32 `weight_scale` per row;

@@ -94,6 +94,8 @@ def _load() -> ctypes.CDLL:
     lib.nvfp4_fp8row_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp, vp]
     lib.nvfp4_rope.argtypes = [ctypes.POINTER(RopeTensor), i32, i64, i64, i64, i32, vp, i32, i64, i32,
                                ctypes.POINTER(ctypes.c_int32), ctypes.c_double, i32, f32, vp]
+    hp = ctypes.POINTER(Heads)
+    lib.nvfp4_attention.argtypes = [hp, hp, hp, hp, i64, i64, i64, i64, i64, i64, i32, vp, f32, vp]
     lib.nvfp4_dequantize.argtypes = [vp, vp, f32, i64, i64, vp, vp]
     lib.nvfp4_w4a16_gemm.argtypes = [vp, vp, vp, i64, i64, i64, f32, vp, vp, vp]
     lib.nvfp4_check_fault.argtypes = []
@@ -107,7 +109,7 @@ def _load() -> ctypes.CDLL:
                  "nvfp4_dequantize", "nvfp4_check_fault", "nvfp4_gemm_tile_shape", "nvfp4_gemm_scaled",
                  "nvfp4_gemm_quant_scaled", "nvfp4_testing_set_grid_wait", "nvfp4_w4a16_gemm",
                  "nvfp4_gemm_plan", "nvfp4_gemm_amax", "nvfp4_quantize_from_amax", "nvfp4_mxfp4_quantize",
-                 "nvfp4_mxfp4_gemm", "nvfp4_rope"):
+                 "nvfp4_mxfp4_gemm", "nvfp4_rope", "nvfp4_attention"):
         getattr(lib, name).restype = ctypes.c_int
     lib.nvfp4_last_error.argtypes = []
     lib.nvfp4_last_error.restype = ctypes.c_char_p
@@ -248,6 +250,13 @@ def nvfp4_rope(tensors: Sequence[RopeTensor], batch: int, tokens: int, head_dim:
     dims = (ctypes.c_int32 * len(axis_dims))(*axis_dims)
     _check(library().nvfp4_rope(arr, len(tensors), batch, tokens, head_dim, dtype, positions, pos_type,
                                 pos_batch_stride, len(axis_dims), dims, theta, flags, eps, stream))
+
+
+def nvfp4_attention(q: Heads, k: Heads, v: Heads, out: Heads, batch: int, q_tokens: int, kv_tokens: int,
+                    q_heads: int, kv_heads: int, head_dim: int, dtype: int, kv_lens: int, scale: float,
+                    stream: int) -> None:
+    _check(library().nvfp4_attention(q, k, v, out, batch, q_tokens, kv_tokens, q_heads, kv_heads, head_dim, dtype,
+                                     kv_lens or None, scale, stream))
 
 
 def nvfp4_dequantize(codes: int, sf: int, g: float, rows: int, K: int, out: int, stream: int) -> None:
@@ -719,6 +728,35 @@ def rope(q, positions, axes: Sequence[int], k=None, theta: float = 10000.0, q_we
                axes, float(theta), ROPE_INTERLEAVED * bool(interleaved) + ROPE_SHARED_LADDER * bool(shared),
                float(eps), _stream(stream))
     return results[0] if k is None else tuple(results)
+
+
+def cross_attention(q, k, v, kv_lens=None, scale: Optional[float] = None, out=None, stream=None):
+    """softmax(scale q k^T) v for bf16 or fp16 heads: queries ``q`` [batch,
+    q_tokens, q_heads, head_dim] over states ``k``, ``v`` [batch, kv_tokens,
+    kv_heads, head_dim] of another length (q_heads a multiple of kv_heads).
+
+    ``kv_lens`` (int32 [batch], on the GPU) gives each entry's valid states,
+    all without it; what the tensors hold behind them does not matter, and an
+    entry without states gets zeros.  ``scale`` is 1 / sqrt(head_dim) by
+    default.  k and v may be views expanded over the batch."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    _need_heads(q, "q", dev=dev)
+    B, Lq, Hq, D = q.shape
+    _need_heads(k, "k", q.dtype, dev=dev)
+    _need_heads(v, "v", q.dtype, k.shape, dev=dev)
+    if k.shape[0] != B or k.shape[3] != D:
+        raise ValueError(f"k must be [{B}, tokens, heads, {D}], got {tuple(k.shape)}")
+    if kv_lens is not None:
+        _need(kv_lens, torch.int32, (B,), "kv_lens", dev=dev)
+    if out is None:
+        out = _empty_on(stream, q.shape, q)
+    else:
+        _need_heads(out, "out", q.dtype, q.shape, dev=dev)
+    nvfp4_attention(_heads(q), _heads(k), _heads(v), _heads(out), B, Lq, k.shape[1], Hq, k.shape[2], D,
+                    DTYPE_FP16 if q.dtype == torch.float16 else DTYPE_BF16, _ptr(kv_lens),
+                    D ** -0.5 if scale is None else float(scale), _stream(stream))
+    return out
 
 
 def swizzle_sf(sf_linear, rows: int, k: int, stream=None):

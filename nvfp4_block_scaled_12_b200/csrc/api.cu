@@ -131,8 +131,8 @@ nvfp4_status make_tmap_nd(CUtensorMap* m, CUtensorMapDataType dt, const void* ba
                           const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw, const char* what) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return fail(NVFP4_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  cuuint64_t d[3], st[2];
-  cuuint32_t bx[3], es[3] = {1, 1, 1};
+  cuuint64_t d[4], st[3];
+  cuuint32_t bx[4], es[4] = {1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     d[i] = dims[i];
     bx[i] = box[i];
@@ -289,6 +289,24 @@ nvfp4_status check_heads(const char* name, const nvfp4_heads& t, int64_t batch, 
                   (long long)head_dim);
   }
   return NVFP4_OK;
+}
+
+// Tensor map of a heads tensor, [head_dim, heads, tokens, batch] with boxes of
+// 64 elements x box_heads x box_tokens.  *bmul: what a batch index counts for
+// (0 when the entries share the tensor).
+nvfp4_status make_heads_tmap(CUtensorMap* m, const nvfp4_heads& t, int64_t batch, int64_t tokens, int64_t heads,
+                             int64_t head_dim, uint32_t box_heads, uint32_t box_tokens, bool fp16, int32_t* bmul,
+                             const char* what) {
+  *bmul = batch > 1 && t.batch_stride != 0 ? 1 : 0;
+  const uint64_t dims[4] = {static_cast<uint64_t>(head_dim), static_cast<uint64_t>(heads),
+                            static_cast<uint64_t>(tokens), static_cast<uint64_t>(*bmul ? batch : 1)};
+  const uint64_t row = static_cast<uint64_t>(head_dim) * 2;  // stands in for a stride that is not used
+  const uint64_t strides[3] = {heads > 1 ? static_cast<uint64_t>(t.head_stride) * 2 : row,
+                               tokens > 1 ? static_cast<uint64_t>(t.token_stride) * 2 : row,
+                               *bmul ? static_cast<uint64_t>(t.batch_stride) * 2 : row};
+  const uint32_t box[4] = {64, box_heads, box_tokens, 1};
+  return make_tmap_nd(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, t.data, 4, dims,
+                      strides, box, CU_TENSOR_MAP_SWIZZLE_128B, what);
 }
 
 // nvfp4_gemm_quant with alpha = fl(alpha * alpha_mul) formed on the device.
@@ -537,6 +555,77 @@ nvfp4_status nvfp4_rope(const nvfp4_rope_tensor* tensors, int32_t n_tensors, int
   cudaError_t e = launch_rope(p, blocks, dtype == NVFP4_DTYPE_FP16, (flags & NVFP4_ROPE_INTERLEAVED) != 0, norm,
                               static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rope launch");
+  return ok();
+}
+
+nvfp4_status nvfp4_attention(const nvfp4_heads* q, const nvfp4_heads* k, const nvfp4_heads* v, const nvfp4_heads* out,
+                             int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads, int64_t kv_heads,
+                             int64_t head_dim, int32_t dtype, const int32_t* kv_lens, float scale, void* stream) {
+  if (!q || !k || !v || !out) return fail(NVFP4_EINVAL, "null pointer");
+  const struct {
+    const char* name;
+    int64_t n, most;
+  } extents[] = {{"batch", batch, kMaxDim},      {"q_tokens", q_tokens, kMaxDim}, {"kv_tokens", kv_tokens, kMaxDim},
+                 {"q_heads", q_heads, 65535},    {"kv_heads", kv_heads, 65535}};
+  for (const auto& x : extents)
+    if (x.n < 1 || x.n > x.most)
+      return fail(NVFP4_EINVAL, "%s=%lld must be in [1, %lld]", x.name, (long long)x.n, (long long)x.most);
+  if (head_dim < 8 || head_dim % 8 != 0 || head_dim > 128)
+    return fail(NVFP4_EINVAL, "head_dim=%lld must be a multiple of 8 in [8, 128]", (long long)head_dim);
+  if (q_heads % kv_heads != 0 || q_heads / kv_heads > 128)
+    return fail(NVFP4_EINVAL, "q_heads=%lld must be a multiple of kv_heads=%lld, at most 128 to each",
+                (long long)q_heads, (long long)kv_heads);
+  if (dtype != NVFP4_DTYPE_BF16 && dtype != NVFP4_DTYPE_FP16) return fail(NVFP4_EINVAL, "unknown dtype %d", dtype);
+  if (!finite_f(scale) || scale <= 0.0f) return fail(NVFP4_EINVAL, "scale must be positive and finite");
+  if (reinterpret_cast<uintptr_t>(kv_lens) % 4 != 0) return fail(NVFP4_EALIGN, "kv_lens must be 4-byte aligned");
+  const struct {
+    const char* name;
+    const nvfp4_heads* t;
+    int64_t tokens, heads;
+  } tensors[] = {{"q", q, q_tokens, q_heads}, {"k", k, kv_tokens, kv_heads}, {"v", v, kv_tokens, kv_heads}};
+  for (const auto& x : tensors) {
+    nvfp4_status st = check_heads(x.name, *x.t, batch, x.tokens, x.heads, head_dim, false);
+    if (st != NVFP4_OK) return st;
+    if ((x.tokens > 1 && x.t->token_stride == 0) || (x.heads > 1 && x.t->head_stride == 0))
+      return fail(NVFP4_EINVAL, "%s: only the batch may share one entry (a stride of 0)", x.name);
+  }
+  nvfp4_status st = check_heads("out", *out, batch, q_tokens, q_heads, head_dim, true);
+  if (st != NVFP4_OK) return st;
+
+  AttentionParams p = {};
+  p.out = out->data;
+  p.out_batch = batch > 1 ? out->batch_stride : 0;
+  p.out_token = q_tokens > 1 ? out->token_stride : 0;
+  p.out_head = q_heads > 1 ? out->head_stride : 0;
+  p.kv_lens = kv_lens;
+  p.q_tokens = static_cast<int32_t>(q_tokens);
+  p.kv_tokens = static_cast<int32_t>(kv_tokens);
+  p.kv_heads = static_cast<int32_t>(kv_heads);
+  p.D = static_cast<int32_t>(head_dim);
+  p.group = static_cast<int32_t>(q_heads / kv_heads);
+  p.tile_tokens = 128 / p.group;
+  p.tile_rows = p.tile_tokens * p.group;
+  p.q_tiles = (p.q_tokens + p.tile_tokens - 1) / p.tile_tokens;
+  p.pairs = (p.q_tiles + 1) / 2;
+  if (batch * kv_heads > INT32_MAX / p.pairs) return fail(NVFP4_EINVAL, "problem too large");
+  p.items = static_cast<int32_t>(batch * kv_heads * p.pairs);
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  const DeviceInfo* dev = nullptr;
+  st = current_device(&dev);
+  if (st != NVFP4_OK) return st;
+  p.split = attention_split(p.items, kv_tokens, dev->num_sms);
+  p.fault = dev->fault;
+  AttentionMaps maps;
+  const bool fp16 = dtype == NVFP4_DTYPE_FP16;
+  st = make_heads_tmap(&maps.q, *q, batch, q_tokens, q_heads, head_dim, static_cast<uint32_t>(p.group),
+                       static_cast<uint32_t>(p.tile_tokens), fp16, &p.q_bmul, "Q");
+  if (st == NVFP4_OK)
+    st = make_heads_tmap(&maps.k, *k, batch, kv_tokens, kv_heads, head_dim, 1, 128, fp16, &p.k_bmul, "K");
+  if (st == NVFP4_OK)
+    st = make_heads_tmap(&maps.v, *v, batch, kv_tokens, kv_heads, head_dim, 1, 128, fp16, &p.v_bmul, "V");
+  if (st != NVFP4_OK) return st;
+  cudaError_t e = launch_attention(maps, p, fp16, static_cast<cudaStream_t>(stream), *dev);
+  if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   return ok();
 }
 

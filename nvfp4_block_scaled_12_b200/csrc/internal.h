@@ -165,4 +165,27 @@ bool rope_plan(RopeParams* p, int64_t tokens, int num_sms, int64_t* blocks);
 cudaError_t launch_rope(const RopeParams& p, int64_t blocks, bool fp16, bool interleaved, bool norm,
                         cudaStream_t stream);
 
+// Attention (csrc/attention.cu).  Strides in elements.
+struct AttentionParams {
+  void* out;
+  int64_t out_batch, out_token, out_head;
+  const int32_t* kv_lens;  // nullable: all kv_tokens states are valid
+  int32_t q_tokens, kv_tokens, kv_heads, D;
+  int32_t group;                    // query heads per K/V head
+  int32_t tile_tokens, tile_rows;   // tokens of a query tile, and its rows (tokens * group, at most 128)
+  int32_t q_tiles, pairs, items;    // query tiles, pairs of them, work items (batch * kv_heads * pairs)
+  int32_t split;                    // CTAs of a cluster that share an item's keys
+  int32_t q_bmul, k_bmul, v_bmul;   // 0: the batch entries share the tensor
+  float scale_log2;
+  unsigned* fault;
+};
+struct AttentionMaps {
+  // [D, heads, tokens, batch], boxes of 64 elements x (group, tile_tokens) or (1, 128)
+  CUtensorMap q, k, v;
+};
+// CTAs that share the keys of one of `items` work items.
+int attention_split(int64_t items, int64_t kv_tokens, int num_sms);
+cudaError_t launch_attention(const AttentionMaps& m, const AttentionParams& p, bool fp16, cudaStream_t stream,
+                             const DeviceInfo& dev);
+
 }  // namespace nvfp4

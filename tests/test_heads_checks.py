@@ -50,7 +50,7 @@ def test_rope_rejects_unaligned_pointers(kw):
 @pytest.fixture
 def calls(monkeypatch):
     rec = []
-    for name in ("nvfp4_rope",):
+    for name in ("nvfp4_rope", "nvfp4_attention"):
         monkeypatch.setattr(F, name, lambda *a, _n=name: rec.append((_n, a)))
     monkeypatch.setattr(F, "_stream", lambda stream: 0)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
@@ -86,6 +86,56 @@ def test_rope_helper(calls):
                 lambda: F.rope(q, empty(9, 2, dtype=torch.int32, dev=1), [32, 32], q_out=qo),
                 lambda: F.rope(q, empty(2, 9, dtype=torch.int32).t(), [32, 32], q_out=qo),
                 lambda: F.rope(empty(2, 0, 4, 64, dtype=BF), empty(0, 2, dtype=torch.int32), [32, 32])):
+        with pytest.raises((TypeError, ValueError)):
+            bad()
+    assert len(calls) == 2
+
+
+def attention_args(**kw):
+    a = dict(q=heads(), k=heads(), v=heads(), out=heads(), batch=2, q_tokens=64, kv_tokens=64, q_heads=8, kv_heads=8,
+             head_dim=64, dtype=0, kv_lens=0, scale=0.125, stream=0)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(batch=0), dict(q_tokens=0), dict(kv_tokens=0), dict(q_heads=0), dict(kv_heads=0), dict(head_dim=0),
+    dict(head_dim=68), dict(head_dim=136), dict(q_heads=8, kv_heads=3), dict(q_heads=258, kv_heads=2, batch=1),
+    dict(dtype=2), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
+    dict(batch=1 << 29, kv_heads=8), dict(q=heads(data=0)), dict(out=heads(data=0)), dict(k=heads(token=4)),
+    dict(v=heads(head=-64)), dict(k=heads(token=0)), dict(q=heads(head=0)), dict(out=heads(batch=0)),
+    dict(out=heads(head=56)), dict(k=heads(batch=1 << 40))])
+def test_attention_rejects_bad_arguments(kw):
+    _expect(F.NVFP4_EINVAL, F.nvfp4_attention, *attention_args(**kw))
+
+
+@pytest.mark.parametrize("kw", [dict(q=heads(data=P + 8)), dict(v=heads(data=P + 2)), dict(out=heads(data=P + 8)),
+                                dict(kv_lens=P + 2)])
+def test_attention_rejects_unaligned_pointers(kw):
+    _expect(F.NVFP4_EALIGN, F.nvfp4_attention, *attention_args(**kw))
+
+
+def test_attention_helper(calls):
+    q, k, v, out = (empty(2, n, h, 64, dtype=BF) for n, h in ((9, 4), (33, 2), (33, 2), (9, 4)))
+    lens = empty(2, dtype=torch.int32)
+    assert F.cross_attention(q, k, v, kv_lens=lens, out=out) is out
+    F.cross_attention(q, k, v, scale=0.3, out=out)
+    (_, a), (_, b) = calls
+    assert a[4:11] == (2, 9, 33, 4, 2, 64, 0) and a[11] and abs(a[12] - 0.125) < 1e-12
+    assert b[11] == 0 and b[12] == 0.3
+    h16 = torch.float16
+    for bad in (lambda: F.cross_attention(q, k, empty(2, 32, 2, 64, dtype=BF), out=out),
+                lambda: F.cross_attention(q, k, empty(2, 33, 2, 64, dtype=h16), out=out),
+                lambda: F.cross_attention(q, empty(3, 33, 2, 64, dtype=BF), empty(3, 33, 2, 64, dtype=BF), out=out),
+                lambda: F.cross_attention(q, empty(2, 33, 2, 72, dtype=BF), empty(2, 33, 2, 72, dtype=BF), out=out),
+                lambda: F.cross_attention(empty(2, 9, 4, 64, dtype=torch.float32), k, v, out=out),
+                lambda: F.cross_attention(q, k, v, kv_lens=empty(3, dtype=torch.int32), out=out),
+                lambda: F.cross_attention(q, k, v, kv_lens=empty(2, dtype=torch.int64), out=out),
+                lambda: F.cross_attention(q, k, v, kv_lens=empty(2, dtype=torch.int32, dev=1), out=out),
+                lambda: F.cross_attention(q, k, v, out=empty(2, 9, 2, 64, dtype=BF)),
+                lambda: F.cross_attention(q, empty(2, 33, 2, 64, dtype=BF, dev=1), v, out=out),
+                lambda: F.cross_attention(q, empty(2, 0, 2, 64, dtype=BF), empty(2, 0, 2, 64, dtype=BF), out=out),
+                lambda: F.cross_attention(q.transpose(2, 3), k, v, out=out)):
         with pytest.raises((TypeError, ValueError)):
             bad()
     assert len(calls) == 2

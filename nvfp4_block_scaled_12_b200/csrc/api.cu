@@ -623,6 +623,10 @@ nvfp4_status nvfp4_attention(const nvfp4_heads* q, const nvfp4_heads* k, const n
     st = make_heads_tmap(&maps.k, *k, batch, kv_tokens, kv_heads, head_dim, 1, 128, fp16, &p.k_bmul, "K");
   if (st == NVFP4_OK)
     st = make_heads_tmap(&maps.v, *v, batch, kv_tokens, kv_heads, head_dim, 1, 128, fp16, &p.v_bmul, "V");
+  int32_t o_bmul = 0;
+  if (st == NVFP4_OK)
+    st = make_heads_tmap(&maps.o, *out, batch, q_tokens, q_heads, head_dim, static_cast<uint32_t>(p.group),
+                         static_cast<uint32_t>(p.tile_tokens), fp16, &o_bmul, "out");
   if (st != NVFP4_OK) return st;
   cudaError_t e = launch_attention(maps, p, fp16, static_cast<cudaStream_t>(stream), *dev);
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");

@@ -9,27 +9,38 @@
 // r % group, so K and V are read once per group.  Per 128-key tile and slot
 //     S  = Q K^T       128 x 128 x DP  tcgen05.mma, Q and K from shared memory
 //     P  = exp2(c S - c m)             softmax warps, S from and P to TMEM
-//     O += P V         128 x DP x 128  tcgen05.mma, P from TMEM (over S), V
-//                                      from shared memory as a transposed operand
-// with c = scale log2 e.  The two slots alternate: the tensor cores work on
-// one while the softmax warps work on the other.
+//     O += P V         128 x DP x 128  tcgen05.mma, P from TMEM, V from shared
+//                                      memory as a transposed operand
+// with c = scale log2 e.
+//
+// TMEM: S | P0 | P1 | O0 | O1, 128 + 64 + 64 + 128 + 128 columns.  The two slots
+// share one S: a softmax warp reads its row's scores into registers at once and
+// hands S back, so the other slot's scores, and then its own next ones, are
+// made while it works on these, and neither product is on its way from one
+// tile to the next.  (With an S of its own per slot, P over it, a slot waited
+// for both products every tile: 231 us for joint attention of 4608 tokens and
+// 24 heads of 128, against 205 us.)
+//
+// Warps (12): 0-3 softmax of slot 0 (one row a thread), 4-7 of slot 1, 8 issues
+// the scores' MMAs, 10 the products', 9 is the TMA producer (11 fills up their
+// warpgroup, whose registers go to the softmax threads: a row's 128 scores stay
+// in registers).  One issuer for both spent longer on its waits and commits
+// than the tensor cores on its MMAs (249 us).  Shared memory: both Q tiles, a
+// ring of K and V tiles, and a panel of O per slot on its way out.
 //
 // The reference m of a row is its first tile's maximum and moves only when a
-// later maximum exceeds it by 2^8 in P (P stays below 2^8, far inside the
-// types' ranges, and the sums in fp32 keep their relative accuracy); only
-// then is O rescaled in TMEM.  S, the maximum, the sum and O are fp32; P is
-// rounded to the type of V for the tensor cores (the sum takes it unrounded,
-// so a row's error from this averages out over its keys).
+// later tile's sum of P exceeds what the type of P holds with room to spare
+// (2^15 in fp16, 2^60 in bf16; a relative accuracy is all that matters below):
+// then the tile is made again with its own maximum, and O is rescaled in TMEM.
+// So only the first tile's maxima are ever taken; P of the others is made at
+// once, and the sum, which is needed anyway, is the check.  S, the maximum, the
+// sum and O are fp32; P is rounded to the type of V for the tensor cores (the
+// sum takes it unrounded, so a row's error from this averages out over its keys).
 //
 // States from kv_lens[b] on contribute nothing whatever they hold: their
 // scores are replaced, not added to, and in the last tile the V rows that the
 // MMA reads beyond them (up to the next multiple of 16 keys) are zeroed in
 // shared memory, since 0 * NaN is NaN.  Keys past the tensor arrive as zeros.
-//
-// Warps (12): 0-3 softmax of slot 0 (one row a thread), 4-7 of slot 1, 8 MMA
-// issuer, 9 TMA producer (10 and 11 fill up their warpgroup, whose registers go
-// to the softmax threads: a row's 128 scores stay in registers).  TMEM: S0 | S1 | O0 | O1, 128 columns each.  Shared
-// memory: both Q tiles and a ring of K and V tiles in their order of use.
 //
 // With fewer items than SMs the keys are split over the CTAs of a cluster:
 // each keeps its own m, sum and O, which are joined through distributed shared
@@ -50,29 +61,79 @@ template <int kDP>
 struct ACfg {
   static constexpr int kPanels = kDP / 64;
   static constexpr uint32_t kTileBytes = kPanels * kPanelBytes;
-  static constexpr int kStages = kDP == 128 ? 5 : 8;
+  static constexpr int kStages = kDP == 128 ? 4 : 8;
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffKv = 2 * kTileBytes;
-  static constexpr uint32_t kOffBar = kOffKv + kStages * kTileBytes;
-  // kv_full, kv_empty per stage; q_full, q_empty, s_full, p_ready, o_full per slot; drain
-  static constexpr uint32_t kNumBars = 2 * kStages + 10 + 1;
+  static constexpr uint32_t kOffOut = kOffKv + kStages * kTileBytes;  // a panel of O on its way out, per slot
+  static constexpr uint32_t kOffBar = kOffOut + 2 * kPanelBytes;
+  // kv_full, kv_empty per stage; q_full, q_empty, s_full, p_ready, pv_done per slot; s_free, two drains
+  static constexpr uint32_t kNumBars = 2 * kStages + 10 + 3;
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
   static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;  // + alignment slack
   // K/V split: a slot's fp32 partial rows (padded to spread them over the
-  // banks) and its maxima and sums, in the idle ring
+  // banks) and its maxima and sums, in the idle ring and what follows it
   static constexpr uint32_t kPartStride = (kDP + 4) * 4;
   static constexpr uint32_t kPartSlot = 128 * kPartStride;
   static constexpr uint32_t kPartMl = 2 * kPartSlot;  // float2 (m, l) [2][128]
-  static_assert(kPartMl + 2 * 128 * 8 <= kStages * kTileBytes, "the partial results fit the ring");
+  static_assert(kOffKv + kPartMl + 2 * 128 * 8 <= kOffBar, "the partial results fit");
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
-constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns of slot 0; slot 1 is 128 further
+// Pairs of every 16 whose exponentials are made by f2_exp2.
+constexpr int kCubic = 0;
+
+// TMEM columns: one S for both slots, P and O of each.
+constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
+constexpr uint32_t kSlotP = 64, kSlotO = 128;
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Packed pairs of floats (the low half first) and their arithmetic.
+__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 2^x of a pair on the FMA pipes, x <= 2^22 (from -125 down: 2^-125).  The
+// special-function unit makes 16 exponentials a clock and SM, which would take
+// a tile as long as its two products take the tensor cores; a share of them is
+// made here instead.  x = n + f with n the nearest whole number, by adding and
+// taking away 1.5 * 2^23, whose sum holds n in its low bits; 2^f by a cubic
+// fitted to the smallest relative error on [-1/2, 1/2] (Remez exchange: 7.5e-5
+// = 2^-13.7, below every rounding of P); n goes into the exponent.
+__device__ __forceinline__ uint64_t f2_exp2(uint64_t x) {
+  constexpr float kBig = 12582912.0f;
+  float a, b;
+  f2_unpack(x, a, b);
+  x = f2_pack(fmaxf(a, -125.0f), fmaxf(b, -125.0f));
+  const uint64_t t = f2_add(x, f2_pack(kBig, kBig));
+  const uint64_t n = f2_add(t, f2_pack(-kBig, -kBig));
+  const uint64_t f = f2_fma(n, f2_pack(-1.0f, -1.0f), x);
+  uint64_t y = f2_fma(f, f2_pack(0.0551716685295105f, 0.0551716685295105f), f2_pack(0.2426111251115799f, 0.2426111251115799f));
+  y = f2_fma(y, f, f2_pack(0.6932609677314758f, 0.6932609677314758f));
+  y = f2_fma(y, f, f2_pack(0.9999280571937561f, 0.9999280571937561f));
+  float ta, tb;
+  f2_unpack(t, ta, tb);
+  f2_unpack(y, a, b);
+  return f2_pack(__uint_as_float(__float_as_uint(a) + (__float_as_uint(ta) << 23)),
+                 __uint_as_float(__float_as_uint(b) + (__float_as_uint(tb) << 23)));
 }
 
 // Two values to the operand type, the first in the low half.
@@ -106,14 +167,38 @@ __device__ __forceinline__ uint64_t sdesc_nmajor_sw128(uint32_t saddr) {
   return d;
 }
 
-// D (TMEM) (+)= A (TMEM, 16-bit pairs) * B (shared memory)
-__device__ __forceinline__ void tc_mma_16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// The MMA warps run their loops as a whole and one elected lane (always the
+// same) issues: the operands are then warp-uniform values in uniform registers.
+// With the loop under `if (lane == 0)` every MMA moved its operands over first,
+// and issuing them took longer than running them.
+
+// D (TMEM) (+)= A (shared memory) * B (shared memory), 16-bit operands
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D (TMEM) (+)= A (TMEM, 16-bit pairs) * B (shared memory)
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
       ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
 
@@ -124,6 +209,29 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uin
       ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
+
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, const void* src, int32_t x, int32_t y, int32_t z,
+                                             int32_t w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];"
+               ::"l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+// Where a step's K and V and the next K are in a ring of S tiles that holds
+// K, V, K, V, ..
+template <int S>
+struct RingPos {
+  int stage = 0;  // this step's K
+  uint32_t phase = 0u;
+  __device__ __forceinline__ int v_stage() const { return stage + 1 < S ? stage + 1 : stage + 1 - S; }
+  __device__ __forceinline__ uint32_t v_phase() const { return stage + 1 < S ? phase : phase ^ 1u; }
+  __device__ __forceinline__ int k_stage() const { return stage + 2 < S ? stage + 2 : stage + 2 - S; }
+  __device__ __forceinline__ uint32_t k_phase() const { return stage + 2 < S ? phase : phase ^ 1u; }
+  __device__ __forceinline__ void next_step() {
+    phase = k_phase();
+    stage = k_stage();
+  }
+};
 
 // One work item as every role sees it.
 struct AttItem {
@@ -151,8 +259,10 @@ __device__ __forceinline__ AttItem att_item(const AttentionParams& p, int item, 
 template <int kDP, bool kFp16>
 __global__ void __launch_bounds__(kAttThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                     const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ AttentionParams p) {
+                     const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_o,
+                     const __grid_constant__ AttentionParams p) {
   using C = ACfg<kDP>;
+  constexpr float kMostSum = kFp16 ? 0x1p15f : 0x1p60f;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -162,8 +272,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   uint64_t* q_empty = q_full + 2;
   uint64_t* s_full = q_empty + 2;
   uint64_t* p_ready = s_full + 2;
-  uint64_t* o_full = p_ready + 2;
-  uint64_t* drain = o_full + 2;
+  uint64_t* pv_done = p_ready + 2;
+  uint64_t* s_free = pv_done + 2;
+  uint64_t* drain = s_free + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const int warp = threadIdx.x >> 5;
@@ -182,16 +293,24 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], 4);  // the slot's four softmax warps
-      mbar_init(&o_full[i], 1);
+      mbar_init(&pv_done[i], 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(s_free, 4);  // the four softmax warps that read S
+    for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
+  // rows of the Q tiles that no query fills (a group that does not divide 128)
+  for (int t = threadIdx.x; t < 2 * C::kPanels * (128 - p.tile_rows) * 8; t += kAttThreads) {
+    const int chunks = (128 - p.tile_rows) * 8, panel = t / chunks, at = t - panel * chunks;
+    *reinterpret_cast<uint4*>(smem + C::kOffQ + panel * kPanelBytes + p.tile_rows * 128 + at * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_async_smem();
   if (warp == 9 && lane == 0) {
     prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
+    prefetch_tmap(&tmap_o);
   }
   if (warp == 8) {
     tmem_alloc(tmem_slot, 512);
@@ -256,83 +375,84 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         if (q_used[i]) mbar_wait(&q_full[i], q_phase[i] ^ 1u, nullptr);
     }
   } else if (warp == 8) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = idesc_16<kFp16>(kAttTile, false);
-      constexpr uint32_t idesc_pv = idesc_16<kFp16>(kDP, true);
-      int64_t e = 0;  // ring entries consumed: K of step s is entry 2s, V is 2s + 1
-      uint32_t q_phase[2] = {0u, 0u}, p_phase[2] = {0u, 0u};
-      // the step whose P V is still to be issued
-      struct {
-        int slots = 0;
-        int64_t v_entry = 0;
-        uint32_t accumulate = 0;
-        int k16 = 0;  // 16-key steps that hold a valid key
-        bool last = false;
-      } pend;
-      auto wait_kv = [&](int64_t entry) {
-        return mbar_wait(&kv_full[entry % S], static_cast<uint32_t>(entry / S) & 1u, abort_flag);
-      };
-      // O_i (+)= P_i V of the pending step
-      auto issue_pv = [&](int i) {
-        if (i >= pend.slots) return true;
-        if (!mbar_wait(&p_ready[i], p_phase[i], abort_flag)) return false;
-        p_phase[i] ^= 1u;
-        if (i == 0 && !wait_kv(pend.v_entry)) return false;
-        tc_fence_after();
-        const uint64_t vd =
-            sdesc_nmajor_sw128(smem_u32(smem + C::kOffKv + static_cast<uint32_t>(pend.v_entry % S) * C::kTileBytes));
-        const uint32_t o = tmem + kColO + i * 128, a = tmem + kColS + i * 128;
-        for (int k = 0; k < pend.k16; ++k)
-          tc_mma_16_ts(o, a + k * 8, vd + k * (2048 >> 4), idesc_pv, (k != 0) ? 1u : pend.accumulate);
-        if (pend.last) tc_commit(&o_full[i]);
-        if (i == pend.slots - 1) tc_commit(&kv_empty[pend.v_entry % S]);
-        return true;
-      };
-      for (int item = first; item < p.items && fault == 0u; item += step) {
-        const AttItem w = att_item(p, item, rank);
-        for (int j = 0; j < w.n; ++j) {
-          bool ok = true;
-          for (int i = 0; i < 2 && ok; ++i) {
-            ok = issue_pv(i);
-            if (!ok || i >= w.slots) continue;
-            if (i == 0) ok = wait_kv(e);
-            if (ok && j == 0) {
-              ok = mbar_wait(&q_full[i], q_phase[i], abort_flag);
-              q_phase[i] ^= 1u;
-            }
-            if (!ok) continue;
-            tc_fence_after();
-            const uint64_t qd = sdesc_kmajor_sw128(smem_u32(smem + C::kOffQ + i * C::kTileBytes));
-            const uint64_t kd =
-                sdesc_kmajor_sw128(smem_u32(smem + C::kOffKv + static_cast<uint32_t>(e % S) * C::kTileBytes));
+    // ------------------------------------------------------------ scores: S = Q_i K
+    constexpr uint32_t idesc = idesc_16<kFp16>(kAttTile, false);
+    RingPos<S> ring;  // of the present step's K
+    uint32_t q_phase[2] = {0u, 0u}, s_phase = 1u;  // (nobody has S at the start)
+    auto wait = [&](uint64_t* bar, uint32_t parity) {  // of the whole warp
+      const bool ok = mbar_wait(bar, parity, abort_flag);
+      __syncwarp();
+      return __all_sync(0xffffffffu, ok) != 0;
+    };
+    for (int item = first; item < p.items && fault == 0u; item += step) {
+      const AttItem w = att_item(p, item, rank);
+      for (int j = 0; j < w.n && fault == 0u; ++j, ring.next_step()) {
+        const uint64_t kd = sdesc_kmajor_sw128(smem_u32(smem + C::kOffKv + ring.stage * C::kTileBytes));
+        bool ok = wait(&kv_full[ring.stage], ring.phase);
+        for (int i = 0; i < w.slots && ok; ++i) {
+          if (j == 0) {
+            ok = wait(&q_full[i], q_phase[i]);
+            q_phase[i] ^= 1u;
+          }
+          ok = ok && wait(s_free, s_phase);  // the last S, the other slot's, has been read
+          s_phase ^= 1u;
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t qd = sdesc_kmajor_sw128(smem_u32(smem + C::kOffQ + i * C::kTileBytes));
 #pragma unroll
-            for (int k = 0; k < kDP / 16; ++k) {
-              const uint64_t off = static_cast<uint64_t>((k / 4) * (kPanelBytes >> 4) + (k % 4) * 2);
-              tc_mma_bf16(tmem + kColS + i * 128, qd + off, kd + off, idesc_qk, k != 0 ? 1u : 0u);
-            }
-            tc_commit(&s_full[i]);
-            if (j == w.n - 1) tc_commit(&q_empty[i]);
-            if (i == w.slots - 1) tc_commit(&kv_empty[e % S]);
+          for (int k = 0; k < kDP / 16; ++k) {
+            const uint64_t off = static_cast<uint64_t>((k / 4) * (kPanelBytes >> 4) + (k % 4) * 2);
+            mma_ss(tmem + kColS, qd + off, kd + off, idesc, k != 0 ? 1u : 0u);
           }
-          if (!ok) {
-            fault = kFaultMmaWait;
-            break;
-          }
-          pend.slots = w.slots;
-          pend.v_entry = e + 1;
-          pend.accumulate = j != 0 ? 1u : 0u;
-          pend.k16 = min(kAttTile, w.len - (w.kt0 + j) * kAttTile + 15) / 16;
-          pend.last = j == w.n - 1;
-          e += 2;
+          commit_elected(&s_full[i]);
+          if (j == w.n - 1) commit_elected(&q_empty[i]);
+          if (i == w.slots - 1) commit_elected(&kv_empty[ring.stage]);
         }
+        if (!ok) fault = kFaultMmaWait;
       }
-      if (fault == 0u && (!issue_pv(0) || !issue_pv(1))) fault = kFaultMmaWait;
-      if (fault != 0u) *abort_flag = 1;
-      // every tcgen05 operation issued must complete before TMEM is released
-      tc_commit(drain);
-      if (!mbar_wait(drain, 0u, nullptr)) fault |= kFaultDrainWait;
     }
+    if (fault != 0u) *abort_flag = 1;
+    // every tcgen05 operation issued must complete before TMEM is released
+    commit_elected(&drain[0]);
+    if (!mbar_wait(&drain[0], 0u, nullptr)) fault |= kFaultDrainWait;
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ products: O_i (+)= P_i V
+    constexpr uint32_t idesc = idesc_16<kFp16>(kDP, true);
+    RingPos<S> ring;
+    uint32_t p_phase[2] = {0u, 0u};
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool ok = mbar_wait(bar, parity, abort_flag);
+      __syncwarp();
+      return __all_sync(0xffffffffu, ok) != 0;
+    };
+    for (int item = first; item < p.items && fault == 0u; item += step) {
+      const AttItem w = att_item(p, item, rank);
+      for (int j = 0; j < w.n && fault == 0u; ++j, ring.next_step()) {
+        const uint64_t vd = sdesc_nmajor_sw128(smem_u32(smem + C::kOffKv + ring.v_stage() * C::kTileBytes));
+        const int k16 = min(kAttTile, w.len - (w.kt0 + j) * kAttTile + 15) / 16;  // 16-key steps with a valid key
+        bool ok = wait(&kv_full[ring.v_stage()], ring.v_phase());
+        for (int i = 0; i < w.slots && ok; ++i) {
+          ok = wait(&p_ready[i], p_phase[i]);
+          p_phase[i] ^= 1u;
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t o = tmem + kColO + i * kSlotO, a = tmem + kColP + i * kSlotP;
+          if (k16 == 8) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mma_ts(o, a + k * 8, vd + k * (2048 >> 4), idesc, (j != 0 || k != 0) ? 1u : 0u);
+          } else {
+            for (int k = 0; k < k16; ++k) mma_ts(o, a + k * 8, vd + k * (2048 >> 4), idesc, (j != 0 || k != 0) ? 1u : 0u);
+          }
+          commit_elected(&pv_done[i]);
+          if (i == w.slots - 1) commit_elected(&kv_empty[ring.v_stage()]);
+        }
+        if (!ok) fault = kFaultMmaWait;
+      }
+    }
+    if (fault != 0u) *abort_flag = 1;
+    commit_elected(&drain[1]);
+    if (!mbar_wait(&drain[1], 0u, nullptr)) fault |= kFaultDrainWait;
     __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax
@@ -343,21 +463,25 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const int i = warp >> 2;  // slot
     const int row = (warp & 3) * 32 + lane;
     const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + kColS + i * 128 + t_lane, t_o = tmem + kColO + i * 128 + t_lane;
+    const uint32_t t_s = tmem + kColS + t_lane, t_p = tmem + kColP + i * kSlotP + t_lane;
+    const uint32_t t_o = tmem + kColO + i * kSlotO + t_lane;
     const float c = p.scale_log2;
-    uint32_t s_phase = 0u, o_phase = 0u;
-    int64_t steps = 0;  // key tiles so far (slot 0 sees every one of the CTA)
+    uint32_t s_phase = 0u, pv_phase = 0u;
+    RingPos<S> ring;  // of this step's K
     auto all_lanes = [&](bool ok) {
       __syncwarp();
       return __all_sync(0xffffffffu, ok) != 0;
     };
     for (int item = first; item < p.items && fault == 0u; item += step) {
       const AttItem w = att_item(p, item, rank);
-      if (i >= w.slots) continue;
+      if (i >= w.slots) {
+        for (int j = 0; j < w.n; ++j) ring.next_step();
+        continue;
+      }
       m_ref = -INFINITY;
       l_sum = 0.0f;
       have = w.n > 0;
-      for (int j = 0; j < w.n; ++j, ++steps) {
+      for (int j = 0; j < w.n; ++j, ring.next_step()) {
         const int valid = w.len - (w.kt0 + j) * kAttTile;  // keys of this tile (more than 128: all)
         if (!all_lanes(mbar_wait(&s_full[i], s_phase, abort_flag))) {
           fault = kFaultEpilogueWait;
@@ -369,6 +493,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         tmem_ld_32x32b_x64(t_s, r);
         tmem_ld_32x32b_x64(t_s + 64, r + 64);
         tmem_ld_wait_n<128>(r);
+        // S is in registers: the next scores, the other slot's, may come
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free);
         if (valid < kAttTile) {
 #pragma unroll
           for (int k = 0; k < 128; ++k)
@@ -376,13 +504,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           if (i == 0 && (valid & 15) != 0) {
             // the V rows from the last valid state to the next multiple of 16
             // keys: zero, whatever they hold (0 * NaN would not be)
-            const int64_t entry = 2 * steps + 1;
-            const bool ok = mbar_wait(&kv_full[entry % S], static_cast<uint32_t>(entry / S) & 1u, abort_flag);
-            if (!all_lanes(ok)) {
+            if (!all_lanes(mbar_wait(&kv_full[ring.v_stage()], ring.v_phase(), abort_flag))) {
               fault = kFaultEpilogueWait;
               break;
             }
-            uint8_t* v = smem + C::kOffKv + static_cast<uint32_t>(entry % S) * C::kTileBytes;
+            uint8_t* v = smem + C::kOffKv + ring.v_stage() * C::kTileBytes;
             const int chunks = (16 - (valid & 15)) * 8;  // 16-byte chunks of a panel's rows
             for (int t = row; t < chunks * C::kPanels; t += 128) {
               const int panel = t / chunks, at = t - panel * chunks;
@@ -391,48 +517,82 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             fence_async_smem();
           }
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto row_max = [&]() {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int k = 0; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(r[k]));
-        const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (j == 0) {
-          m_ref = m_tile;
-        } else {
-          const bool moves = (m_tile - m_ref) * c > 8.0f;
-          if (__any_sync(0xffffffffu, moves)) {
-            // (S of this tile is complete, and it was issued after the
-            // previous tile's P V: nobody else touches O)
-            const float f = moves ? exp2_approx((m_ref - m_tile) * c) : 1.0f;
-            if (moves) m_ref = m_tile;
-            l_sum *= f;
-#pragma unroll 1
-            for (int d = 0; d < kDP; d += 32) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(t_o + d, o);
-              tmem_ld_wait(o);
+          for (int k = 0; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(r[k]));
+          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        };
+        // P of the keys from 64 h on with the present reference, two to a word
+        uint32_t pk[32];
+        auto make_p = [&](int h) {
+          const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-m_ref * c, -m_ref * c);
+          uint64_t sum[2] = {0u, 0u};
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st_32x32b_x16(t_o + d, *reinterpret_cast<const uint32_t(*)[16]>(o));
-              tmem_st_32x32b_x16(t_o + d + 16, *reinterpret_cast<const uint32_t(*)[16]>(o + 16));
+          for (int k = 0; k < 32; ++k) {
+            const uint64_t x =
+                f2_fma(f2_pack(__uint_as_float(r[64 * h + 2 * k]), __uint_as_float(r[64 * h + 2 * k + 1])), c2, mc2);
+            float a, b;
+            uint64_t e;
+            if (k % 16 < kCubic) {
+              e = f2_exp2(x);
+              f2_unpack(e, a, b);
+            } else {
+              f2_unpack(x, a, b);
+              a = exp2_approx(a);
+              b = exp2_approx(b);
+              e = f2_pack(a, b);
             }
-          }
-        }
-        const float mc = -m_ref * c;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {  // 32 keys: 16 TMEM columns of P
-          uint32_t pk[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float a = exp2_approx(fmaf(__uint_as_float(r[g * 32 + 2 * k]), c, mc));
-            const float b = exp2_approx(fmaf(__uint_as_float(r[g * 32 + 2 * k + 1]), c, mc));
-            sum[(2 * k) & 3] += a;
-            sum[(2 * k + 1) & 3] += b;
+            sum[k & 1] = f2_add(sum[k & 1], e);
             pk[k] = pack2<kFp16>(a, b);
           }
-          tmem_st_32x32b_x16(t_s + g * 16, pk);
+          float a, b;
+          f2_unpack(f2_add(sum[0], sum[1]), a, b);
+          return a + b;
+        };
+        auto store_p = [&](int h) {
+          tmem_st_32x32b_x16(t_p + 32 * h, *reinterpret_cast<const uint32_t(*)[16]>(pk));
+          tmem_st_32x32b_x16(t_p + 32 * h + 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16));
+        };
+        if (j == 0) m_ref = row_max();
+        float tile_sum = make_p(0);
+        if (j > 0) {
+          // the last tile's product has read P (and O is complete up to it)
+          if (!all_lanes(mbar_wait(&pv_done[i], pv_phase, abort_flag))) {
+            fault = kFaultEpilogueWait;
+            break;
+          }
+          pv_phase ^= 1u;
+          tc_fence_after();
         }
-        l_sum += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        store_p(0);
+        tile_sum += make_p(1);
+        if (j > 0) {
+          const bool moves = tile_sum > kMostSum;
+          if (__any_sync(0xffffffffu, moves)) {
+            // rare: the tile's maximum becomes the reference, O and the sum so
+            // far are scaled down to it, and P is made again
+            const float m_new = moves ? row_max() : m_ref;
+            const float f = moves ? exp2_approx((m_ref - m_new) * c) : 1.0f;
+            m_ref = m_new;
+            l_sum *= f;
+#pragma unroll 1
+            for (int d = 0; d < kDP; d += 16) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(t_o + d, o);
+              tmem_ld_wait_n<16>(o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st_32x32b_x16(t_o + d, o);
+            }
+            tmem_st_wait();
+            tile_sum = make_p(0);
+            store_p(0);
+            tile_sum += make_p(1);
+          }
+        }
+        store_p(1);
+        l_sum += tile_sum;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -440,43 +600,53 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       }
       if (fault != 0u) break;
       if (w.n > 0) {
-        if (!all_lanes(mbar_wait(&o_full[i], o_phase, abort_flag))) {
+        if (!all_lanes(mbar_wait(&pv_done[i], pv_phase, abort_flag))) {
           fault = kFaultEpilogueWait;
           break;
         }
-        o_phase ^= 1u;
+        pv_phase ^= 1u;
         tc_fence_after();
       }
       if (p.split > 1) break;  // one item; joined below
-      // ---- O / sum to the output row (zeros where there are no states)
-      const int token = (w.tile0 + i) * p.tile_tokens + row / p.group;
-      const bool write = row < p.tile_rows && token < p.q_tokens;
+      // ---- O / sum through shared memory, 64 columns at a time, to the output
+      // (zeros where there are no states).  One row a thread straight to global
+      // memory took 4200 clocks a tile: every store touched 32 lines.
       const float inv = w.n > 0 ? 1.0f / l_sum : 0.0f;
-      uint16_t* out = static_cast<uint16_t*>(p.out) + w.b * p.out_batch + static_cast<int64_t>(token) * p.out_token +
-                      static_cast<int64_t>(w.hk * p.group + row % p.group) * p.out_head;
+      uint8_t* panel = smem + C::kOffOut + i * kPanelBytes;
 #pragma unroll 1
-      for (int d = 0; d < p.D; d += 32) {
-        uint32_t o[32];
-        if (w.n > 0) {
-          tmem_ld_32x32b_x32(t_o + d, o);
-          tmem_ld_wait(o);
-        } else {
+      for (int d = 0; d < p.D; d += 64) {
+        if (row == 0) bulk_wait_read<0>();  // the last panel has left
+        named_barrier_sync(2 + i, 128);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0u;
+        for (int h = 0; h < 2; ++h) {
+          uint32_t o[32];
+          if (w.n > 0) {
+            tmem_ld_32x32b_x32(t_o + d + 32 * h, o);
+            tmem_ld_wait(o);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[e] = pack2<kFp16>(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+            *reinterpret_cast<uint4*>(panel + row * 128 + (((4 * h + k) ^ (row & 7)) * 16)) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
         }
-        if (!write) continue;
-        uint32_t y[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          y[k] = pack2<kFp16>(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-          if (d + 8 * h < p.D)
-            *reinterpret_cast<uint4*>(out + d + 8 * h) = make_uint4(y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]);
+        fence_async_smem();
+        named_barrier_sync(2 + i, 128);
+        if (row == 0) {  // (rows past the queries and columns past the width are clipped)
+          tma_store_4d(&tmap_o, panel, d, w.hk * p.group, (w.tile0 + i) * p.tile_tokens, w.b);
+          bulk_commit();
+        }
       }
       tc_fence_before();  // these reads of O come before the next item's P V
     }
     if (fault != 0u) *abort_flag = 1;
+    if (row == 0) bulk_wait<0>();
     if (p.split > 1) {
       // ------------------------------------------------------------ join of the key ranges
       // Every role of this CTA is done, so the ring is idle: each softmax thread
@@ -584,7 +754,7 @@ cudaError_t launch(const AttentionMaps& m, const AttentionParams& p, cudaStream_
   // a split item has a cluster of its own; otherwise one CTA per SM takes items in turn
   const int ctas = p.split > 1 ? p.items * p.split : (p.items < dev.num_sms ? p.items : dev.num_sms);
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
-  err = cudaLaunchKernelEx(&cfg, kernel, m.q, m.k, m.v, p);
+  err = cudaLaunchKernelEx(&cfg, kernel, m.q, m.k, m.v, m.o, p);
   if (err != cudaSuccess) return err;
   return cudaGetLastError();
 }

@@ -180,8 +180,8 @@ struct AttentionParams {
   unsigned* fault;
 };
 struct AttentionMaps {
-  // [D, heads, tokens, batch], boxes of 64 elements x (group, tile_tokens) or (1, 128)
-  CUtensorMap q, k, v;
+  // [D, heads, tokens, batch], boxes of 64 elements x (group, tile_tokens) for Q and O, (1, 128) for K and V
+  CUtensorMap q, k, v, o;
 };
 // CTAs that share the keys of one of `items` work items.
 int attention_split(int64_t items, int64_t kv_tokens, int num_sms);

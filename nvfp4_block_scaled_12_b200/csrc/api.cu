@@ -613,7 +613,6 @@ nvfp4_status nvfp4_attention(const nvfp4_heads* q, const nvfp4_heads* k, const n
   const DeviceInfo* dev = nullptr;
   st = current_device(&dev);
   if (st != NVFP4_OK) return st;
-  p.split = attention_split(p.items, kv_tokens, dev->num_sms);
   p.fault = dev->fault;
   AttentionMaps maps;
   const bool fp16 = dtype == NVFP4_DTYPE_FP16;

@@ -42,16 +42,20 @@
 // MMA reads beyond them (up to the next multiple of 16 keys) are zeroed in
 // shared memory, since 0 * NaN is NaN.  Keys past the tensor arrive as zeros.
 //
-// With fewer items than SMs the keys are split over the CTAs of a cluster:
-// each keeps its own m, sum and O, which are joined through distributed shared
-// memory in the order of the ranks (no workspace, no atomics, and the same
-// result every time).
+// With fewer items than SMs the keys are split over the CTAs of a cluster, and
+// where all queries of a K/V head fit one tile the two slots take its key tiles
+// in turn: each part keeps its own m, sum and O, and they are joined through
+// distributed shared memory in a fixed order (no workspace, no atomics, and the
+// same result every time).
+#include <atomic>
+
 #include "internal.h"
 
 namespace nvfp4 {
 
 namespace {
 
+constexpr int kAttMaxSplit = 8;  // the portable cluster size
 constexpr int kAttTile = 128;  // query rows of a slot, keys of a tile
 constexpr int kAttThreads = 384;  // three warpgroups: softmax of each slot, producer and MMA
 constexpr uint32_t kPanelBytes = 128 * 128;  // 128 rows of 64 elements, 128-byte swizzle
@@ -78,9 +82,6 @@ struct ACfg {
   static_assert(kOffKv + kPartMl + 2 * 128 * 8 <= kOffBar, "the partial results fit");
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
-
-// Pairs of every 16 whose exponentials are made by f2_exp2.
-constexpr int kCubic = 0;
 
 // TMEM columns: one S for both slots, P and O of each.
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
@@ -111,31 +112,6 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// 2^x of a pair on the FMA pipes, x <= 2^22 (from -125 down: 2^-125).  The
-// special-function unit makes 16 exponentials a clock and SM, which would take
-// a tile as long as its two products take the tensor cores; a share of them is
-// made here instead.  x = n + f with n the nearest whole number, by adding and
-// taking away 1.5 * 2^23, whose sum holds n in its low bits; 2^f by a cubic
-// fitted to the smallest relative error on [-1/2, 1/2] (Remez exchange: 7.5e-5
-// = 2^-13.7, below every rounding of P); n goes into the exponent.
-__device__ __forceinline__ uint64_t f2_exp2(uint64_t x) {
-  constexpr float kBig = 12582912.0f;
-  float a, b;
-  f2_unpack(x, a, b);
-  x = f2_pack(fmaxf(a, -125.0f), fmaxf(b, -125.0f));
-  const uint64_t t = f2_add(x, f2_pack(kBig, kBig));
-  const uint64_t n = f2_add(t, f2_pack(-kBig, -kBig));
-  const uint64_t f = f2_fma(n, f2_pack(-1.0f, -1.0f), x);
-  uint64_t y = f2_fma(f, f2_pack(0.0551716685295105f, 0.0551716685295105f), f2_pack(0.2426111251115799f, 0.2426111251115799f));
-  y = f2_fma(y, f, f2_pack(0.6932609677314758f, 0.6932609677314758f));
-  y = f2_fma(y, f, f2_pack(0.9999280571937561f, 0.9999280571937561f));
-  float ta, tb;
-  f2_unpack(t, ta, tb);
-  f2_unpack(y, a, b);
-  return f2_pack(__uint_as_float(__float_as_uint(a) + (__float_as_uint(ta) << 23)),
-                 __uint_as_float(__float_as_uint(b) + (__float_as_uint(tb) << 23)));
-}
-
 // Two values to the operand type, the first in the low half.
 template <bool kFp16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -237,6 +213,7 @@ struct RingPos {
 struct AttItem {
   int b, hk, tile0;    // batch entry, K/V head, first query tile
   int slots;           // 1 or 2 query tiles
+  bool shared;         // both slots share the one tile and take its key tiles in turn
   int len;             // valid states of the batch entry
   int kt0, n;          // first key tile and key tiles of this CTA
 };
@@ -249,6 +226,7 @@ __device__ __forceinline__ AttItem att_item(const AttentionParams& p, int item, 
   w.b = bh / p.kv_heads;
   w.tile0 = 2 * pair;
   w.slots = min(2, p.q_tiles - w.tile0);
+  w.shared = p.join != 0 && p.q_tiles == 1;
   w.len = p.kv_lens != nullptr ? min(max(__ldg(p.kv_lens + w.b), 0), p.kv_tokens) : p.kv_tokens;
   const int tiles = (w.len + kAttTile - 1) / kAttTile;
   w.kt0 = static_cast<int>(static_cast<int64_t>(tiles) * rank / p.split);
@@ -322,6 +300,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   const uint32_t tmem = *tmem_slot;
   unsigned fault = 0u;
 
+  // every thread of the item's CTAs
+  auto sync_cluster = [&]() {
+    if (p.split > 1)
+      cluster_sync();
+    else
+      named_barrier_sync(1, kAttThreads);
+  };
   if (warp >= 8) {
     // (launched with 384 x 168 registers: 88 + 2 x 208 = 3 x 168)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
@@ -389,24 +374,26 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       for (int j = 0; j < w.n && fault == 0u; ++j, ring.next_step()) {
         const uint64_t kd = sdesc_kmajor_sw128(smem_u32(smem + C::kOffKv + ring.stage * C::kTileBytes));
         bool ok = wait(&kv_full[ring.stage], ring.phase);
-        for (int i = 0; i < w.slots && ok; ++i) {
+        const int i0 = w.shared ? (j & 1) : 0, i1 = w.shared ? i0 + 1 : w.slots;
+        for (int i = i0; i < i1 && ok; ++i) {
+          const int qi = w.shared ? 0 : i;
           if (j == 0) {
-            ok = wait(&q_full[i], q_phase[i]);
-            q_phase[i] ^= 1u;
+            ok = wait(&q_full[qi], q_phase[qi]);
+            q_phase[qi] ^= 1u;
           }
           ok = ok && wait(s_free, s_phase);  // the last S, the other slot's, has been read
           s_phase ^= 1u;
           if (!ok) break;
           tc_fence_after();
-          const uint64_t qd = sdesc_kmajor_sw128(smem_u32(smem + C::kOffQ + i * C::kTileBytes));
+          const uint64_t qd = sdesc_kmajor_sw128(smem_u32(smem + C::kOffQ + qi * C::kTileBytes));
 #pragma unroll
           for (int k = 0; k < kDP / 16; ++k) {
             const uint64_t off = static_cast<uint64_t>((k / 4) * (kPanelBytes >> 4) + (k % 4) * 2);
             mma_ss(tmem + kColS, qd + off, kd + off, idesc, k != 0 ? 1u : 0u);
           }
           commit_elected(&s_full[i]);
-          if (j == w.n - 1) commit_elected(&q_empty[i]);
-          if (i == w.slots - 1) commit_elected(&kv_empty[ring.stage]);
+          if (j == w.n - 1) commit_elected(&q_empty[qi]);
+          if (i == i1 - 1) commit_elected(&kv_empty[ring.stage]);
         }
         if (!ok) fault = kFaultMmaWait;
       }
@@ -432,7 +419,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         const uint64_t vd = sdesc_nmajor_sw128(smem_u32(smem + C::kOffKv + ring.v_stage() * C::kTileBytes));
         const int k16 = min(kAttTile, w.len - (w.kt0 + j) * kAttTile + 15) / 16;  // 16-key steps with a valid key
         bool ok = wait(&kv_full[ring.v_stage()], ring.v_phase());
-        for (int i = 0; i < w.slots && ok; ++i) {
+        const int i0 = w.shared ? (j & 1) : 0, i1 = w.shared ? i0 + 1 : w.slots;
+        const bool adds = w.shared ? j > 1 : j > 0;  // not the slot's first product
+        for (int i = i0; i < i1 && ok; ++i) {
           ok = wait(&p_ready[i], p_phase[i]);
           p_phase[i] ^= 1u;
           if (!ok) break;
@@ -440,12 +429,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           const uint32_t o = tmem + kColO + i * kSlotO, a = tmem + kColP + i * kSlotP;
           if (k16 == 8) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) mma_ts(o, a + k * 8, vd + k * (2048 >> 4), idesc, (j != 0 || k != 0) ? 1u : 0u);
+            for (int k = 0; k < 8; ++k) mma_ts(o, a + k * 8, vd + k * (2048 >> 4), idesc, (adds || k != 0) ? 1u : 0u);
           } else {
-            for (int k = 0; k < k16; ++k) mma_ts(o, a + k * 8, vd + k * (2048 >> 4), idesc, (j != 0 || k != 0) ? 1u : 0u);
+            for (int k = 0; k < k16; ++k) mma_ts(o, a + k * 8, vd + k * (2048 >> 4), idesc, (adds || k != 0) ? 1u : 0u);
           }
           commit_elected(&pv_done[i]);
-          if (i == w.slots - 1) commit_elected(&kv_empty[ring.v_stage()]);
+          if (i == i1 - 1) commit_elected(&kv_empty[ring.v_stage()]);
         }
         if (!ok) fault = kFaultMmaWait;
       }
@@ -474,14 +463,16 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     };
     for (int item = first; item < p.items && fault == 0u; item += step) {
       const AttItem w = att_item(p, item, rank);
-      if (i >= w.slots) {
+      if (i >= w.slots && !w.shared) {
         for (int j = 0; j < w.n; ++j) ring.next_step();
         continue;
       }
+      const int j0 = w.shared ? i : 0;  // this slot's first key tile
       m_ref = -INFINITY;
       l_sum = 0.0f;
-      have = w.n > 0;
+      have = w.n > j0;
       for (int j = 0; j < w.n; ++j, ring.next_step()) {
+        if (w.shared && (j & 1) != i) continue;
         const int valid = w.len - (w.kt0 + j) * kAttTile;  // keys of this tile (more than 128: all)
         if (!all_lanes(mbar_wait(&s_full[i], s_phase, abort_flag))) {
           fault = kFaultEpilogueWait;
@@ -501,7 +492,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 #pragma unroll
           for (int k = 0; k < 128; ++k)
             if (k >= valid) r[k] = 0xFF800000u;  // -inf
-          if (i == 0 && (valid & 15) != 0) {
+          if ((i == 0 || w.shared) && (valid & 15) != 0) {
             // the V rows from the last valid state to the next multiple of 16
             // keys: zero, whatever they hold (0 * NaN would not be)
             if (!all_lanes(mbar_wait(&kv_full[ring.v_stage()], ring.v_phase(), abort_flag))) {
@@ -533,17 +524,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             const uint64_t x =
                 f2_fma(f2_pack(__uint_as_float(r[64 * h + 2 * k]), __uint_as_float(r[64 * h + 2 * k + 1])), c2, mc2);
             float a, b;
-            uint64_t e;
-            if (k % 16 < kCubic) {
-              e = f2_exp2(x);
-              f2_unpack(e, a, b);
-            } else {
-              f2_unpack(x, a, b);
-              a = exp2_approx(a);
-              b = exp2_approx(b);
-              e = f2_pack(a, b);
-            }
-            sum[k & 1] = f2_add(sum[k & 1], e);
+            f2_unpack(x, a, b);
+            a = exp2_approx(a);
+            b = exp2_approx(b);
+            sum[k & 1] = f2_add(sum[k & 1], f2_pack(a, b));
             pk[k] = pack2<kFp16>(a, b);
           }
           float a, b;
@@ -554,9 +538,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           tmem_st_32x32b_x16(t_p + 32 * h, *reinterpret_cast<const uint32_t(*)[16]>(pk));
           tmem_st_32x32b_x16(t_p + 32 * h + 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16));
         };
-        if (j == 0) m_ref = row_max();
+        if (j == j0) m_ref = row_max();
         float tile_sum = make_p(0);
-        if (j > 0) {
+        if (j > j0) {
           // the last tile's product has read P (and O is complete up to it)
           if (!all_lanes(mbar_wait(&pv_done[i], pv_phase, abort_flag))) {
             fault = kFaultEpilogueWait;
@@ -567,7 +551,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         }
         store_p(0);
         tile_sum += make_p(1);
-        if (j > 0) {
+        if (j > j0) {
           const bool moves = tile_sum > kMostSum;
           if (__any_sync(0xffffffffu, moves)) {
             // rare: the tile's maximum becomes the reference, O and the sum so
@@ -599,7 +583,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         if (lane == 0) mbar_arrive(&p_ready[i]);
       }
       if (fault != 0u) break;
-      if (w.n > 0) {
+      if (have) {
         if (!all_lanes(mbar_wait(&pv_done[i], pv_phase, abort_flag))) {
           fault = kFaultEpilogueWait;
           break;
@@ -607,11 +591,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         pv_phase ^= 1u;
         tc_fence_after();
       }
-      if (p.split > 1) break;  // one item; joined below
+      if (p.join) break;  // one item; joined below
       // ---- O / sum through shared memory, 64 columns at a time, to the output
       // (zeros where there are no states).  One row a thread straight to global
       // memory took 4200 clocks a tile: every store touched 32 lines.
-      const float inv = w.n > 0 ? 1.0f / l_sum : 0.0f;
+      const float inv = have ? 1.0f / l_sum : 0.0f;
       uint8_t* panel = smem + C::kOffOut + i * kPanelBytes;
 #pragma unroll 1
       for (int d = 0; d < p.D; d += 64) {
@@ -620,7 +604,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t o[32];
-          if (w.n > 0) {
+          if (have) {
             tmem_ld_32x32b_x32(t_o + d + 32 * h, o);
             tmem_ld_wait(o);
           } else {
@@ -647,7 +631,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     }
     if (fault != 0u) *abort_flag = 1;
     if (row == 0) bulk_wait<0>();
-    if (p.split > 1) {
+    if (p.join) {
       // ------------------------------------------------------------ join of the key ranges
       // Every role of this CTA is done, so the ring is idle: each softmax thread
       // leaves its row's O (not normalised), reference and sum there.  Then the
@@ -658,7 +642,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       tc_fence_after();
       uint8_t* part = smem + C::kOffKv;
       const AttItem w = att_item(p, first, rank);
-      if (i < w.slots) {
+      if (i < w.slots || w.shared) {
         *reinterpret_cast<float2*>(part + C::kPartMl + (i * 128 + row) * 8) = make_float2(m_ref, l_sum);
         uint8_t* dst = part + i * C::kPartSlot + row * C::kPartStride;
 #pragma unroll 1
@@ -676,7 +660,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             *reinterpret_cast<uint4*>(dst + d * 4 + k * 16) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
       }
-      cluster_sync();
+      sync_cluster();
       if (*abort_flag == 0) {
         const int groups = p.D / 8;
         const int rows0 = min(p.tile_rows, (p.q_tokens - w.tile0 * p.tile_tokens) * p.group);
@@ -685,17 +669,23 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           const int rr = u / groups, g = u - rr * groups;
           const int i = rr >= rows0 ? 1 : 0;
           const int row = rr - (i ? rows0 : 0);
+          // the row's parts: one per rank, or two where the slots shared the tile
+          const int per_rank = w.shared ? 2 : 1;
+          auto part_at = [&](uint32_t base, uint32_t slot_bytes, int t) {
+            const uint32_t a = base + (w.shared ? static_cast<uint32_t>(t & 1) * slot_bytes : 0u);
+            return peer_smem(a, static_cast<uint32_t>(t / per_rank));
+          };
           const uint32_t ml = smem_u32(part + C::kPartMl + (i * 128 + row) * 8);
           const uint32_t src = smem_u32(part + i * C::kPartSlot + row * C::kPartStride + g * 32);
           float m = -INFINITY;
-          for (int s = 0; s < p.split; ++s) m = fmaxf(m, ld_shared_cluster_f2(peer_smem(ml, s)).x);
+          for (int t = 0; t < p.split * per_rank; ++t) m = fmaxf(m, ld_shared_cluster_f2(part_at(ml, 128 * 8, t)).x);
           float l = 0.0f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          for (int s = 0; s < p.split; ++s) {
-            const float2 x = ld_shared_cluster_f2(peer_smem(ml, s));
+          for (int t = 0; t < p.split * per_rank; ++t) {
+            const float2 x = ld_shared_cluster_f2(part_at(ml, 128 * 8, t));
             if (x.x == -INFINITY) continue;  // no states in that range
             const float f = exp2_approx((x.x - m) * p.scale_log2);
             l = fmaf(x.y, f, l);
-            const uint32_t at = peer_smem(src, s);
+            const uint32_t at = part_at(src, C::kPartSlot, t);
             const float4 a = ld_shared_cluster_f4(at), b = ld_shared_cluster_f4(at + 16);
             v[0] = fmaf(a.x, f, v[0]);
             v[1] = fmaf(a.y, f, v[1]);
@@ -717,11 +707,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       }
     }
   }
-  if (warp >= 8 && p.split > 1) {  // the join's two barriers
+  if (warp >= 8 && p.join) {  // the join's two barriers
     __syncwarp();
     tc_fence_before();
     named_barrier_sync(1, kAttThreads);
-    cluster_sync();
+    sync_cluster();
   }
   if (fault != 0u && lane == 0 && p.fault != nullptr) atomicOr(p.fault, fault);
   tc_fence_before();
@@ -734,12 +724,62 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   }
 }
 
+// Clusters of `split` CTAs that the device holds at once (0: it cannot).
 template <int kDP, bool kFp16>
-cudaError_t launch(const AttentionMaps& m, const AttentionParams& p, cudaStream_t stream, const DeviceInfo& dev) {
+int resident_clusters(int split, const DeviceInfo& dev) {
+  static std::atomic<int> cache[kMaxDevices][kAttMaxSplit + 1];  // the count plus one; the same for any two threads
+  int n = cache[dev.device][split].load(std::memory_order_relaxed) - 1;
+  if (n < 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kAttThreads, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms / split * split), 1, 1);
+    cfg.dynamicSmemBytes = ACfg<kDP>::kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, attention_kernel<kDP, kFp16>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    cache[dev.device][split].store(n + 1, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+template <int kDP, bool kFp16>
+cudaError_t launch(const AttentionMaps& m, AttentionParams p, cudaStream_t stream, const DeviceInfo& dev) {
   using C = ACfg<kDP>;
   auto kernel = attention_kernel<kDP, kFp16>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (err != cudaSuccess) return err;
+  // How an item is shared out, by its cost in key tiles of one slot: whole
+  // items in turn, one CTA per SM (kTurnCost for an item's ends), or items with
+  // CTAs of their own, in waves of the clusters that fit, each taking its share
+  // of the key tiles (two at a time where the slots share the only query tile)
+  // plus kJoinCost for the start and the join.
+  constexpr int kTurnCost = 1, kJoinCost = 3;
+  const int tiles = (p.kv_tokens + kAttTile - 1) / kAttTile;
+  const int at_once = p.q_tiles == 1 ? 2 : 1;  // key tiles that a joined item's CTA has in work
+  auto waves = [](int n, int fit) { return static_cast<int64_t>((n + fit - 1) / fit); };
+  p.split = 1;
+  p.join = 0;
+  int64_t best = waves(p.items, dev.num_sms) * (tiles + kTurnCost);
+  for (int split = at_once == 2 ? 1 : 2; split <= kAttMaxSplit && split * at_once <= tiles; ++split) {
+    if (split > 1 && p.items > dev.num_sms / 2) break;
+    const int fit = split > 1 ? resident_clusters<kDP, kFp16>(split, dev) : dev.num_sms;
+    if (fit == 0) continue;
+    const int64_t cost = waves(p.items, fit) * ((tiles + split * at_once - 1) / (split * at_once) + kJoinCost);
+    if (cost < best) {
+      best = cost;
+      p.split = split;
+      p.join = 1;
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kAttThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmemBytes;
@@ -751,8 +791,8 @@ cudaError_t launch(const AttentionMaps& m, const AttentionParams& p, cudaStream_
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.split > 1 ? 1 : 0;
-  // a split item has a cluster of its own; otherwise one CTA per SM takes items in turn
-  const int ctas = p.split > 1 ? p.items * p.split : (p.items < dev.num_sms ? p.items : dev.num_sms);
+  if (p.items > INT32_MAX / p.split) return cudaErrorInvalidConfiguration;
+  const int ctas = p.join ? p.items * p.split : (p.items < dev.num_sms ? p.items : dev.num_sms);
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
   err = cudaLaunchKernelEx(&cfg, kernel, m.q, m.k, m.v, m.o, p);
   if (err != cudaSuccess) return err;
@@ -760,13 +800,6 @@ cudaError_t launch(const AttentionMaps& m, const AttentionParams& p, cudaStream_
 }
 
 }  // namespace
-
-int attention_split(int64_t items, int64_t kv_tokens, int num_sms) {
-  const int64_t tiles = (kv_tokens + kAttTile - 1) / kAttTile;
-  int split = 1;
-  while (split < 8 && split * 2 <= tiles && items * split * 2 <= num_sms) split *= 2;
-  return split;
-}
 
 cudaError_t launch_attention(const AttentionMaps& m, const AttentionParams& p, bool fp16, cudaStream_t stream,
                              const DeviceInfo& dev) {

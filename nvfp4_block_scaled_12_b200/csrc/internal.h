@@ -174,7 +174,8 @@ struct AttentionParams {
   int32_t group;                    // query heads per K/V head
   int32_t tile_tokens, tile_rows;   // tokens of a query tile, and its rows (tokens * group, at most 128)
   int32_t q_tiles, pairs, items;    // query tiles, pairs of them, work items (batch * kv_heads * pairs)
-  int32_t split;                    // CTAs of a cluster that share an item's keys
+  int32_t split;                    // CTAs of a cluster that share an item's keys (set by the launch)
+  int32_t join;                     // the items' parts are joined at the end: each has CTAs of its own (set by the launch)
   int32_t q_bmul, k_bmul, v_bmul;   // 0: the batch entries share the tensor
   float scale_log2;
   unsigned* fault;
@@ -183,8 +184,6 @@ struct AttentionMaps {
   // [D, heads, tokens, batch], boxes of 64 elements x (group, tile_tokens) for Q and O, (1, 128) for K and V
   CUtensorMap q, k, v, o;
 };
-// CTAs that share the keys of one of `items` work items.
-int attention_split(int64_t items, int64_t kv_tokens, int num_sms);
 cudaError_t launch_attention(const AttentionMaps& m, const AttentionParams& p, bool fp16, cudaStream_t stream,
                              const DeviceInfo& dev);
 

@@ -299,39 +299,47 @@ def nvfp4_last_error() -> str:
 # torch-tensor helpers (outputs allocated with torch on the input's device)
 # --------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module  # (an import statement on every call costs more than the lookup)
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream) -> int:
+    if stream is not None:
+        return int(stream.cuda_stream)
+    # the current stream's handle without a Stream object around it (7 us of a 22 us call)
     torch = _torch()
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t) -> int:
-    return 0 if t is None else int(t.data_ptr())
+    return 0 if t is None else t.data_ptr()
 
 
 def _need(t, dtype, shape, name, min_numel=None, dev=None):
     """``t`` must be a contiguous CUDA tensor of ``dtype`` on the current
     device, of ``shape`` (if given) and with at least ``min_numel`` elements
     (if given): the library reads and writes through its raw pointer."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if min_numel is not None and t.numel() < min_numel:
         raise ValueError(f"{name} holds {t.numel()} elements, {min_numel} needed")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    dev = torch.cuda.current_device() if dev is None else dev
-    if t.device.index != dev:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if t.device.index != (torch.cuda.current_device() if dev is None else dev):
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:"
+                         f"{torch.cuda.current_device() if dev is None else dev}")
 
 
 def _need_nvfp4(t, name, rows=None, k=None, dev=None):
@@ -516,14 +524,17 @@ class MXFP4Tensor:
     k: int
 
 
-def _need_mxfp4(t, name, rows=None, k=None, dev=None):
-    rows = t.rows if rows is None else rows
-    k = t.k if k is None else k
+def _mxfp4_sf_bytes(rows, k):
+    """``nvfp4_mxfp4_sf_bytes`` without the call: rows padded to 128, scale columns to 4."""
+    return (rows + 127) // 128 * 128 * ((k // 32 + 3) // 4 * 4)
+
+
+def _need_mxfp4(t, name, rows, k, dev):
     torch = _torch()
-    if (t.rows, t.k) != (rows, k):
+    if t.rows != rows or t.k != k:
         raise ValueError(f"{name} is [{t.rows}, {t.k}], [{rows}, {k}] needed")
     _need(t.codes, torch.uint8, None, f"{name}.codes", rows * k // 2, dev=dev)
-    _need(t.sf, torch.uint8, None, f"{name}.sf", nvfp4_mxfp4_sf_bytes(rows, k), dev=dev)
+    _need(t.sf, torch.uint8, None, f"{name}.sf", _mxfp4_sf_bytes(rows, k), dev=dev)
 
 
 def quantize_mxfp4(x, out: Optional[MXFP4Tensor] = None, stream=None) -> MXFP4Tensor:
@@ -533,11 +544,11 @@ def quantize_mxfp4(x, out: Optional[MXFP4Tensor] = None, stream=None) -> MXFP4Te
     M, K = x.shape
     _need(x, torch.bfloat16, None, "x", dev=dev)
     if out is None:
-        out = MXFP4Tensor(torch.empty(M, K // 2, dtype=torch.uint8, device=x.device),
-                          torch.empty(nvfp4_mxfp4_sf_bytes(M, K), dtype=torch.uint8, device=x.device), M, K)
+        out = MXFP4Tensor(_empty_on(stream, (M, K // 2), x, torch.uint8),
+                          _empty_on(stream, (_mxfp4_sf_bytes(M, K),), x, torch.uint8), M, K)
     else:
-        _need_mxfp4(out, "out", M, K, dev=dev)
-    nvfp4_mxfp4_quantize(_ptr(x), M, K, _ptr(out.codes), _ptr(out.sf), _stream(stream))
+        _need_mxfp4(out, "out", M, K, dev)
+    nvfp4_mxfp4_quantize(x.data_ptr(), M, K, out.codes.data_ptr(), out.sf.data_ptr(), _stream(stream))
     return out
 
 
@@ -548,15 +559,16 @@ def gemm_mxfp4(a: MXFP4Tensor, b: MXFP4Tensor, bias=None, alpha: float = 1.0, y=
     if a.k != b.k:
         raise ValueError("K mismatch")
     M, N, K = a.rows, b.rows, a.k
-    _need_mxfp4(a, "a", dev=dev)
-    _need_mxfp4(b, "b", dev=dev)
+    _need_mxfp4(a, "a", M, K, dev)
+    _need_mxfp4(b, "b", N, K, dev)
     if bias is not None:
         _need(bias, torch.bfloat16, (N,), "bias", dev=dev)
     if y is None:
-        y = torch.empty(M, N, dtype=torch.bfloat16, device=a.codes.device)
-    _need(y, torch.bfloat16, (M, N), "y", dev=dev)
-    nvfp4_mxfp4_gemm(_ptr(a.codes), _ptr(a.sf), _ptr(b.codes), _ptr(b.sf), M, N, K, float(alpha), _ptr(bias),
-                     _ptr(y), _stream(stream))
+        y = _empty_on(stream, (M, N), a.codes, torch.bfloat16)
+    else:
+        _need(y, torch.bfloat16, (M, N), "y", dev=dev)
+    nvfp4_mxfp4_gemm(a.codes.data_ptr(), a.sf.data_ptr(), b.codes.data_ptr(), b.sf.data_ptr(), M, N, K, float(alpha),
+                     _ptr(bias), y.data_ptr(), _stream(stream))
     return y
 
 
@@ -651,18 +663,18 @@ def linear_w4a16(x, w: NVFP4Tensor, bias=None, y=None, stream=None):
     return y
 
 
-def _need_heads(t, name, dtype=None, shape=None, dev=None):
+def _need_heads(t, name, dev, dtype=None, shape=None):
     """``t`` must be a bf16 or fp16 CUDA tensor [batch, tokens, heads,
     head_dim] on the current device with contiguous heads; the library checks
     the other strides, which may be any multiple of 8."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype if dtype is not None else t.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"{name} must be {dtype or 'bfloat16 or float16'}, got {t.dtype}")
-    if t.dim() != 4 or 0 in t.shape:
+    if t.dim() != 4 or t.numel() == 0:
         raise ValueError(f"{name} must be [batch, tokens, heads, head_dim], none of them 0, got {tuple(t.shape)}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.stride(3) != 1:
         raise ValueError(f"{name}'s heads must be contiguous")
@@ -675,13 +687,12 @@ def _heads(t) -> Heads:
     return Heads(t.data_ptr(), sb, st, sh)
 
 
-def _empty_on(stream, shape, like):
-    """A new tensor of ``like``'s type, owned by the stream that writes it."""
-    torch = _torch()
+def _empty_on(stream, shape, like, dtype=None):
+    """A new tensor on ``like``'s device (of its type, or ``dtype``), owned by the stream that writes it."""
     if stream is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
+    with _torch().cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def rope(q, positions, axes: Sequence[int], k=None, theta: float = 10000.0, q_weight=None, k_weight=None,
@@ -699,7 +710,7 @@ def rope(q, positions, axes: Sequence[int], k=None, theta: float = 10000.0, q_we
     the results (the inputs themselves, to work in place)."""
     torch = _torch()
     dev = torch.cuda.current_device()
-    _need_heads(q, "q", dev=dev)
+    _need_heads(q, "q", dev)
     B, L, _, D = q.shape
     if k is None and (k_weight is not None or k_out is not None):
         raise ValueError("k_weight and k_out need k")
@@ -708,13 +719,13 @@ def rope(q, positions, axes: Sequence[int], k=None, theta: float = 10000.0, q_we
         if x is None:
             continue
         if name == "k":
-            _need_heads(x, name, q.dtype, (B, L, x.shape[2] if x.dim() == 4 else 0, D), dev=dev)
+            _need_heads(x, name, dev, q.dtype, (B, L, x.shape[2] if x.dim() == 4 else 0, D))
         if weight is not None:
             _need(weight, q.dtype, (D,), f"{name}_weight", dev=dev)
         if out is None:
             out = _empty_on(stream, x.shape, x)
         else:
-            _need_heads(out, f"{name}_out", q.dtype, x.shape, dev=dev)
+            _need_heads(out, f"{name}_out", dev, q.dtype, x.shape)
         results.append(out)
         args.append(RopeTensor(_heads(x), _heads(out), x.shape[2], _ptr(weight)))
     if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.float32):
@@ -741,10 +752,10 @@ def cross_attention(q, k, v, kv_lens=None, scale: Optional[float] = None, out=No
     default.  k and v may be views expanded over the batch."""
     torch = _torch()
     dev = torch.cuda.current_device()
-    _need_heads(q, "q", dev=dev)
+    _need_heads(q, "q", dev)
     B, Lq, Hq, D = q.shape
-    _need_heads(k, "k", q.dtype, dev=dev)
-    _need_heads(v, "v", q.dtype, k.shape, dev=dev)
+    _need_heads(k, "k", dev, q.dtype)
+    _need_heads(v, "v", dev, q.dtype, k.shape)
     if k.shape[0] != B or k.shape[3] != D:
         raise ValueError(f"k must be [{B}, tokens, heads, {D}], got {tuple(k.shape)}")
     if kv_lens is not None:
@@ -752,7 +763,7 @@ def cross_attention(q, k, v, kv_lens=None, scale: Optional[float] = None, out=No
     if out is None:
         out = _empty_on(stream, q.shape, q)
     else:
-        _need_heads(out, "out", q.dtype, q.shape, dev=dev)
+        _need_heads(out, "out", dev, q.dtype, q.shape)
     nvfp4_attention(_heads(q), _heads(k), _heads(v), _heads(out), B, Lq, k.shape[1], Hq, k.shape[2], D,
                     DTYPE_FP16 if q.dtype == torch.float16 else DTYPE_BF16, _ptr(kv_lens),
                     D ** -0.5 if scale is None else float(scale), _stream(stream))

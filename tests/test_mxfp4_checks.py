@@ -12,6 +12,8 @@ from tests.test_binding_checks import empty
                                          (5, 16, 0), (5, 48, 0)])
 def test_sf_bytes(rows, k, want):
     assert F.nvfp4_mxfp4_sf_bytes(rows, k) == want
+    if want:
+        assert F._mxfp4_sf_bytes(rows, k) == want
 
 
 def test_entry_points_reject_bad_arguments():

@@ -524,7 +524,8 @@ nvfp4_status nvfp4_rope(const nvfp4_rope_tensor* tensors, int32_t n_tensors, int
                         tokens > 1 ? t.out.token_stride : 0,
                         t.heads > 1 ? t.out.head_stride : 0,
                         t.norm_weight,
-                        static_cast<int32_t>(t.heads)};
+                        static_cast<int32_t>(t.heads),
+                        0};
     norm |= t.norm_weight != nullptr;
   }
   p.positions = positions;

@@ -147,6 +147,7 @@ struct RopeTensor {
   int64_t in_batch, in_token, in_head, out_batch, out_token, out_head;
   const void* weight;  // RMS norm weight [D], nullable
   int32_t heads;
+  int32_t heads_per_unit;
 };
 struct RopeParams {
   RopeTensor t[2];  // the second one with heads == 0 when there is none
@@ -156,8 +157,8 @@ struct RopeParams {
   int32_t L, D, R;
   int32_t n_axes, first_pair[kRopeMaxAxes];
   int32_t pos_float;
-  int32_t group, heads_per_unit, parts0, units_per_token;
-  float eps;
+  int32_t group, heads_per_unit, parts0, units_per_token;  // heads_per_unit: the larger of the two tensors'
+  float eps, inv_d;
   double turns[kRopeMaxPairs];  // a pair's turns per position: f / 2 pi
 };
 // Fills the launch shape for `tokens` = B * L; false when the grid is too large.

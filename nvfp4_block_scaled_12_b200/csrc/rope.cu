@@ -8,16 +8,20 @@
 // halves (i, i + R/2); elements from R on pass through.
 //
 // The kernel is bound by memory: 2 bytes read and 2 written per element.  A
-// group of 2^n >= D/8 lanes owns one token and up to `heads_per_unit` heads of
-// it; a lane owns the same four pairs (eight elements) of every head, so the
-// four sines and cosines are worked out once for all of them and a row's norm
-// is a shuffle within the group.  Lanes load four heads before they use the
-// first, 16 bytes each (two 8-byte halves in the half layout).
+// group of 2^n >= D/8 lanes owns one token and up to 24 heads of it; a lane
+// owns the same four pairs (eight elements) of every head, so the four sines
+// and cosines are worked out once for all of them and a row's norm is a shuffle
+// within the group.  Lanes load the next four heads before they use the last
+// four, 16 bytes each (two 8-byte halves in the half layout), and four blocks
+// fit an SM.  4608 tokens x 48 heads x 128 with the norms: 24.8 us back to back
+// (4.6 TB/s); 30940 tokens x 24 heads x 128: 61.7 us (6.2 TB/s, 0.94 of a copy).
 //
 // The angle is reduced in 64 bits: t = pos * (f_i / 2 pi) turns, of which only
-// t - rint(t) goes on to sincospif in 32 bits, so a position of a million
-// costs no accuracy (in 32 bits its angle would be off by 0.03).  Sums of
-// squares, the norm and the rotation are 32-bit; the result is rounded once.
+// t - rint(t) goes on in 32 bits, so a position of a million costs no accuracy
+// (in 32 bits its angle would be off by 0.03).  Its sine and cosine are the
+// hardware's (within 2^-20.9 on [-pi, pi], far below the 16-bit rounding of the
+// result; sincospif was a third of the instructions).  Sums of squares, the
+// norm and the rotation are 32-bit; the result is rounded once.
 #include <math.h>
 
 #include "internal.h"
@@ -28,51 +32,38 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ void from_f32(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void from_f32(float v, __half& o) { o = __float2half_rn(v); }
-
-// Eight elements of a row: 16 bytes at `lo`, or 8 bytes at `lo` and 8 at `hi`.
-template <typename T>
-struct alignas(16) Eight {
-  T e[8];
-};
-
-template <typename T>
-__device__ __forceinline__ Eight<T> load_eight(const T* row, int lo, int hi, bool split) {
-  union {
-    uint4 u;
-    uint2 h[2];
-    Eight<T> e;
-  } v;
-  if (split) {
-    v.h[0] = *reinterpret_cast<const uint2*>(row + lo);
-    v.h[1] = *reinterpret_cast<const uint2*>(row + hi);
-  } else {
-    v.u = *reinterpret_cast<const uint4*>(row + lo);
+// Two 16-bit elements of a word to floats and back, rounded to nearest.
+template <bool kFp16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (kFp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+template <bool kFp16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (kFp16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
-  return v.e;
+  return pack_bf16x2(lo, hi);
 }
 
-template <typename T>
-__device__ __forceinline__ void store_eight(T* row, int lo, int hi, bool split, const Eight<T>& x) {
-  union {
-    uint4 u;
-    uint2 h[2];
-    Eight<T> e;
-  } v;
-  v.e = x;
-  if (split) {
-    *reinterpret_cast<uint2*>(row + lo) = v.h[0];
-    *reinterpret_cast<uint2*>(row + hi) = v.h[1];
+// Eight elements of a row: 16 bytes at element `lo`, or 8 bytes there and 8 at `hi`.
+__device__ __forceinline__ uint4 load_eight(const uint16_t* row, int lo, int hi, bool split) {
+  if (!split) return *reinterpret_cast<const uint4*>(row + lo);
+  const uint2 a = *reinterpret_cast<const uint2*>(row + lo), b = *reinterpret_cast<const uint2*>(row + hi);
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store_eight(uint16_t* row, int lo, int hi, bool split, uint4 v) {
+  if (!split) {
+    *reinterpret_cast<uint4*>(row + lo) = v;
   } else {
-    *reinterpret_cast<uint4*>(row + lo) = v.u;
+    *reinterpret_cast<uint2*>(row + lo) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2*>(row + hi) = make_uint2(v.z, v.w);
   }
 }
 
-template <typename T, bool kInterleaved, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+template <bool kFp16, bool kInterleaved, bool kNorm>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ double turns[kRopeMaxPairs];  // f_i / 2 pi
   for (int i = threadIdx.x; i < p.R / 2; i += kRopeThreads) turns[i] = p.turns[i];
   __syncthreads();
@@ -84,8 +75,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int part = u - token * p.units_per_token;
   const int which = part >= p.parts0 ? 1 : 0;
   const RopeTensor& t = p.t[which];
-  const int head0 = (part - (which ? p.parts0 : 0)) * p.heads_per_unit;
-  const int nh = min(p.heads_per_unit, t.heads - head0);
+  const int head0 = (part - (which ? p.parts0 : 0)) * t.heads_per_unit;
+  const int nh = live ? min(t.heads_per_unit, t.heads - head0) : 0;
   const int b = token / p.L, l = token - b * p.L;
 
   // this lane's elements of every head
@@ -93,6 +84,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const bool split = !kInterleaved && rotary;
   const int lo = split ? lane * 4 : lane * 8;
   const int hi = p.R / 2 + lane * 4;
+  const uint16_t* in = static_cast<const uint16_t*>(t.in) + b * t.in_batch + l * t.in_token + head0 * t.in_head;
+  uint16_t* out = static_cast<uint16_t*>(t.out) + b * t.out_batch + l * t.out_token + head0 * t.out_head;
+  uint4 next[4];
+  auto load_from = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (h0 + i < nh) next[i] = load_eight(in + (h0 + i) * t.in_head, lo, hi, split);
+  };
+  load_from(0);
 
   float cs[4], sn[4];
 #pragma unroll
@@ -111,75 +111,85 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
       const double pos = p.pos_float ? static_cast<double>(static_cast<const float*>(p.positions)[pos0 + axis])
                                      : static_cast<double>(static_cast<const int32_t*>(p.positions)[pos0 + axis]);
       const double turn = pos * turns[pair];
-      sincospif(2.0f * static_cast<float>(turn - rint(turn)), &sn[j], &cs[j]);
+      __sincosf(6.2831853f * static_cast<float>(turn - rint(turn)), &sn[j], &cs[j]);
     }
   }
   float w[8];
-  if (kNorm) {
+  const bool normed = kNorm && t.weight != nullptr;
+  if (normed) {
+    const uint4 x = live ? load_eight(static_cast<const uint16_t*>(t.weight), lo, hi, split) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 1.0f;
-    if (live && t.weight != nullptr) {
-      const Eight<T> x = load_eight(static_cast<const T*>(t.weight), lo, hi, split);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = to_f32(x.e[j]);
+    for (int j = 0; j < 4; ++j) {
+      const float2 v = unpack2<kFp16>(xw[j]);
+      w[2 * j] = v.x;
+      w[2 * j + 1] = v.y;
     }
   }
-  const T* in = static_cast<const T*>(t.in) + b * t.in_batch + l * t.in_token + head0 * t.in_head;
-  T* out = static_cast<T*>(t.out) + b * t.out_batch + l * t.out_token + head0 * t.out_head;
 
   // every lane of a warp takes the same number of turns: the shuffles below need them all
   for (int h0 = 0; h0 < p.heads_per_unit; h0 += 4) {
-    Eight<T> x[4];
+    uint4 x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (live && h0 + i < nh) x[i] = load_eight(in + (h0 + i) * t.in_head, lo, hi, split);
+    for (int i = 0; i < 4; ++i) x[i] = next[i];
+    load_from(h0 + 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool use = live && h0 + i < nh;
+      const bool use = h0 + i < nh;
+      const uint32_t xw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = use ? to_f32(x[i].e[j]) : 0.0f;
+      for (int j = 0; j < 4; ++j) {
+        const float2 e = unpack2<kFp16>(xw[j]);
+        v[2 * j] = e.x;
+        v[2 * j + 1] = e.y;
+      }
       if (kNorm) {
         float ss = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+        ss = use ? ss : 0.0f;  // (lanes past the width take part with nothing)
         for (int o = p.group >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (t.weight != nullptr) {
-          const float r = rsqrtf(ss / static_cast<float>(p.D) + p.eps);
+        if (normed) {
+          const float r = rsqrtf(ss * p.inv_d + p.eps);
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] *= r * w[j];
         }
       }
       if (!use) continue;
-      Eight<T> y;
-      if (rotary) {
+      uint32_t y[4];
+      if (kInterleaved || !rotary) {
+        // (lanes that pass through have cosines of 1 and sines of 0)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int ia = kInterleaved ? 2 * j : j, ib = kInterleaved ? 2 * j + 1 : j + 4;
-          from_f32(v[ia] * cs[j] - v[ib] * sn[j], y.e[ia]);
-          from_f32(v[ia] * sn[j] + v[ib] * cs[j], y.e[ib]);
-        }
+        for (int j = 0; j < 4; ++j)
+          y[j] = rotary ? pack2<kFp16>(v[2 * j] * cs[j] - v[2 * j + 1] * sn[j], v[2 * j] * sn[j] + v[2 * j + 1] * cs[j])
+                        : pack2<kFp16>(v[2 * j], v[2 * j + 1]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) from_f32(v[j], y.e[j]);
+        for (int j = 0; j < 2; ++j) {
+          y[j] = pack2<kFp16>(v[2 * j] * cs[2 * j] - v[2 * j + 4] * sn[2 * j],
+                              v[2 * j + 1] * cs[2 * j + 1] - v[2 * j + 5] * sn[2 * j + 1]);
+          y[j + 2] = pack2<kFp16>(v[2 * j] * sn[2 * j] + v[2 * j + 4] * cs[2 * j],
+                                  v[2 * j + 1] * sn[2 * j + 1] + v[2 * j + 5] * cs[2 * j + 1]);
+        }
       }
-      store_eight(out + (h0 + i) * t.out_head, lo, hi, split, y);
+      store_eight(out + (h0 + i) * t.out_head, lo, hi, split, make_uint4(y[0], y[1], y[2], y[3]));
     }
   }
 }
 
-template <typename T>
+template <bool kFp16>
 cudaError_t launch(const RopeParams& p, unsigned blocks, bool interleaved, bool norm, cudaStream_t stream) {
   if (interleaved) {
     if (norm)
-      rope_kernel<T, true, true><<<blocks, kRopeThreads, 0, stream>>>(p);
+      rope_kernel<kFp16, true, true><<<blocks, kRopeThreads, 0, stream>>>(p);
     else
-      rope_kernel<T, true, false><<<blocks, kRopeThreads, 0, stream>>>(p);
+      rope_kernel<kFp16, true, false><<<blocks, kRopeThreads, 0, stream>>>(p);
   } else {
     if (norm)
-      rope_kernel<T, false, true><<<blocks, kRopeThreads, 0, stream>>>(p);
+      rope_kernel<kFp16, false, true><<<blocks, kRopeThreads, 0, stream>>>(p);
     else
-      rope_kernel<T, false, false><<<blocks, kRopeThreads, 0, stream>>>(p);
+      rope_kernel<kFp16, false, false><<<blocks, kRopeThreads, 0, stream>>>(p);
   }
   return cudaGetLastError();
 }
@@ -189,28 +199,34 @@ cudaError_t launch(const RopeParams& p, unsigned blocks, bool interleaved, bool 
 bool rope_plan(RopeParams* p, int64_t tokens, int num_sms, int64_t* blocks) {
   p->group = 1;
   while (p->group * 8 < p->D) p->group *= 2;
-  const int h0 = p->t[0].heads, h1 = p->t[1].heads;
-  // Heads of one unit: eight share their sines and cosines when that leaves
-  // every SM two blocks' worth of units, fewer where the units would be too
-  // few to keep the memory busy.
-  int hpu = 8;
-  int64_t units = 0;
-  for (;; hpu /= 2) {
-    p->parts0 = (h0 + hpu - 1) / hpu;
-    p->units_per_token = p->parts0 + (h1 + hpu - 1) / hpu;
-    units = tokens * p->units_per_token;
-    if (hpu == 1 || units * p->group >= static_cast<int64_t>(num_sms) * 2 * kRopeThreads) break;
+  p->inv_d = 1.0f / static_cast<float>(p->D);
+  // Heads of one unit: up to 24 share their sines and cosines where that leaves
+  // every SM two blocks' worth of units, fewer where the units would be too few
+  // to keep the memory busy.  (At most 24 / 12 / 8 / 6 heads: 24.8 / 24.7 / 26.8 /
+  // 33 us for 48 heads of 4608 tokens, L2-cold 26.7 / 28.7 / 30.8 / 34.8.)
+  for (int most = 24;; most /= 2) {
+    int parts[2] = {0, 0};
+    p->heads_per_unit = 0;
+    for (int i = 0; i < 2; ++i) {
+      RopeTensor& t = p->t[i];
+      if (t.heads == 0) continue;
+      parts[i] = (t.heads + most - 1) / most;
+      t.heads_per_unit = (t.heads + parts[i] - 1) / parts[i];
+      p->heads_per_unit = t.heads_per_unit > p->heads_per_unit ? t.heads_per_unit : p->heads_per_unit;
+    }
+    p->parts0 = parts[0];
+    p->units_per_token = parts[0] + parts[1];
+    p->units = tokens * p->units_per_token;
+    if (most == 1 || p->units * p->group >= static_cast<int64_t>(num_sms) * 2 * kRopeThreads) break;
   }
-  p->heads_per_unit = hpu;
-  p->units = units;
-  *blocks = (units * p->group + kRopeThreads - 1) / kRopeThreads;
-  return units <= INT32_MAX && *blocks <= INT32_MAX;
+  *blocks = (p->units * p->group + kRopeThreads - 1) / kRopeThreads;
+  return p->units <= INT32_MAX && *blocks <= INT32_MAX;
 }
 
 cudaError_t launch_rope(const RopeParams& p, int64_t blocks, bool fp16, bool interleaved, bool norm,
                         cudaStream_t stream) {
   const unsigned n = static_cast<unsigned>(blocks);
-  return fp16 ? launch<__half>(p, n, interleaved, norm, stream) : launch<__nv_bfloat16>(p, n, interleaved, norm, stream);
+  return fp16 ? launch<true>(p, n, interleaved, norm, stream) : launch<false>(p, n, interleaved, norm, stream);
 }
 
 }  // namespace nvfp4

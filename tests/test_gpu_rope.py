@@ -4,10 +4,11 @@ layouts, ladders, norms, strides, far and fractional positions, in place.
 Tolerance: one rounding to the type (half a step, eps / 2 of the value, and
 half of fp16's smallest subnormal step) plus 2^-17 of |a| + |b|.  The latter
 covers the 32-bit part, in units of u = 2^-24, as a relative error of each of
-the two terms: sincospif within 4 u and its argument within 3.2 u rad, three
-roundings of the rotation; a norm's sum of squares passes 8 + 5 additions, so
-it is within 13 u, half of that after the root, which adds 4 u for rsqrtf, 1 u
-for the mean and 2 u for the products: below 32 u = 2^-19 in all.  A position
+the two terms: the hardware's sine and cosine within 2^-20.9 = 8.6 u, their
+argument within 3.2 u rad and its product with 2 pi within 3.2 u, three roundings
+of the rotation; a norm's sum of squares passes 8 + 5 additions, so it is within
+13 u, half of that after the root, which adds 4 u for rsqrtf, 2 u for the mean
+and 2 u for the products: below 64 u = 2^-18 in all.  A position
 of 2^31 adds its own 64-bit error, 2^31 * 2^-52 rad = 2^-21, on both sides."""
 import numpy as np
 import pytest

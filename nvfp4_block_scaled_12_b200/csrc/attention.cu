@@ -47,8 +47,6 @@
 // in turn: each part keeps its own m, sum and O, and they are joined through
 // distributed shared memory in a fixed order (no workspace, no atomics, and the
 // same result every time).
-#include <atomic>
-
 #include "internal.h"
 
 namespace nvfp4 {
@@ -755,7 +753,8 @@ template <int kDP, bool kFp16>
 cudaError_t launch(const AttentionMaps& m, AttentionParams p, cudaStream_t stream, const DeviceInfo& dev) {
   using C = ACfg<kDP>;
   auto kernel = attention_kernel<kDP, kFp16>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static SmemLimit limit;
+  cudaError_t err = limit.raise(kernel, C::kSmemBytes, dev.device);
   if (err != cudaSuccess) return err;
   // How an item is shared out, by its cost in key tiles of one slot: whole
   // items in turn, one CTA per SM (kTurnCost for an item's ends), or items with

@@ -51,8 +51,6 @@
 // Every barrier wait is bounded (see mbar_wait); a role that gives up sets
 // the CTA's abort flag and the device fault word, lets the copies it issued
 // land, and the CTA still reaches the final barrier and frees its TMEM.
-#include <atomic>
-
 #include "internal.h"
 
 namespace nvfp4 {
@@ -261,6 +259,9 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16, kMx4>::kT
   __syncthreads();
   if (kCG == 2 || p.k_split > 1) cluster_sync();  // the peer's barriers are initialised before anyone signals them
   tc_fence_after();
+  // MXFP4 is launched before the kernel in front of it, its quantizer as a
+  // rule, has ended: everything up to here touched no global memory
+  if constexpr (kMx4) wait_for_previous_kernel();
   const uint32_t tmem_base = *tmem_slot;
   unsigned fault = 0u;
 
@@ -1032,26 +1033,30 @@ template <int kCG, int kBN, int kAcc, bool kFused, bool kMx, bool kRow = false, 
 cudaError_t launch(const GemmTensorMaps& m, const GemmParams& p, cudaStream_t stream, const DeviceInfo& dev) {
   using C = Cfg<kCG, kBN, kAcc, kMx, kRow, kW16, kMx4>;
   auto kernel = gemm_nvf4_kernel<kCG, kBN, kAcc, kFused, kMx, kRow, kW16, kMx4>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static SmemLimit limit;
+  cudaError_t err = limit.raise(kernel, C::kSmemBytes, dev.device);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(C::kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  // the cluster dimension, and MXFP4's early launch (its kernel waits for the
+  // one before it where it first needs that one's results)
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kCG;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kCG == 2 ? 1 : 0;
+  cfg.numAttrs = kMx4 ? 2 : (kCG == 2 || p.k_split > 1) ? 1 : 0;  // (clusters of one: no cluster launch)
   if (p.k_split > 1) {
     // K split: one tile per cluster of kCG * k_split CTAs (at most 8, the
     // portable cluster size); the clusters are independent, so they need not
     // all be resident at once
     if (C::kWide || kFused || kMx || kCG * p.k_split > 8) return cudaErrorInvalidConfiguration;
     attr[0].val.clusterDim.x = static_cast<unsigned>(kCG * p.k_split);
-    cfg.numAttrs = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(p.num_tiles * kCG * p.k_split), 1, 1);
     err = cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.sfa, m.sfb, m.y, p);
     if (err != cudaSuccess) return err;
@@ -1066,8 +1071,10 @@ cudaError_t launch(const GemmTensorMaps& m, const GemmParams& p, cudaStream_t st
     int n = dev.num_sms / kCG;
     if (kCG == 2) {
       cfg.gridDim = dim3(static_cast<unsigned>(2 * n), 1, 1);
+      cudaLaunchConfig_t query = cfg;
+      query.numAttrs = 1;  // the cluster alone
       int clusters = 0;
-      if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0 && clusters < n)
+      if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &query) == cudaSuccess && clusters > 0 && clusters < n)
         n = clusters;
     }
     max_groups = n;

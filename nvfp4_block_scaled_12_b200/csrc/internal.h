@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "device.cuh"
 #include "nvfp4.h"
 
@@ -12,6 +14,21 @@ namespace nvfp4 {
 
 // Devices the per-device caches of the library cover (device index < this).
 constexpr int kMaxDevices = 64;
+
+// Whether a kernel's dynamic shared memory limit has been raised, per device
+// (the call that raises it is not free, and the limit stays).  One per kernel
+// instance; two host threads that race raise it to the same value.
+struct SmemLimit {
+  std::atomic<bool> raised[kMaxDevices];
+  template <typename Kernel>
+  cudaError_t raise(Kernel kernel, uint32_t bytes, int device) {
+    if (raised[device].load(std::memory_order_relaxed)) return cudaSuccess;
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (err == cudaSuccess) raised[device].store(true, std::memory_order_relaxed);
+    return err;
+  }
+};
 
 struct DeviceInfo {
   int device = -1;

@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(QCfg<kRows>::kThreads, 1)
     fence_mbar_init();
   }
   __syncthreads();
+  if constexpr (kFormat == QFormat::kMxfp4) launch_dependents();  // the GEMM that follows may set itself up
   unsigned fault = 0u;
   // This CTA's tiles are blockIdx.x + j * gridDim.x, j = 0 .. my_tiles-1.
   // The ring carries a sequence of n_seq loads, entry jj = 4i + g going to
@@ -385,7 +386,8 @@ cudaError_t launch_q(const CUtensorMap& tmap_x, const void* x, int64_t M, int64_
   const int64_t n_tiles = tiles_m * tiles_k;
   const int grid = static_cast<int>(n_tiles < dev.num_sms ? n_tiles : dev.num_sms);
   auto kernel = quantize_kernel<kDynamic, kFormat, kRows>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::kSmemBytes);
+  static SmemLimit limit;
+  cudaError_t err = limit.raise(kernel, Q::kSmemBytes, dev.device);
   if (err != cudaSuccess) return err;
   if (!kDynamic) {
     kernel<<<grid, Q::kThreads, Q::kSmemBytes, stream>>>(tmap_x, M, K, g, codes, sf, tiles_k, n_tiles, dev.fault,
@@ -422,7 +424,8 @@ cudaError_t launch_q_amax(const CUtensorMap& tmap_x, int64_t M, int64_t K, uint8
   const int64_t n_tiles = tiles_m * tiles_k;
   const int grid = static_cast<int>(n_tiles < dev.num_sms ? n_tiles : dev.num_sms);
   auto kernel = quantize_kernel<false, QFormat::kNvfp4, kRows>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::kSmemBytes);
+  static SmemLimit limit;
+  cudaError_t err = limit.raise(kernel, Q::kSmemBytes, dev.device);
   if (err != cudaSuccess) return err;
   kernel<<<grid, Q::kThreads, Q::kSmemBytes, stream>>>(tmap_x, M, K, 0.0f, codes, sf, tiles_k, n_tiles, dev.fault, dyn);
   return cudaGetLastError();

@@ -168,14 +168,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void commit_elected(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "elect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
-}
-
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int32_t x, int32_t y,
                                             int32_t z, int32_t w) {
   asm volatile(
@@ -389,16 +381,16 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             const uint64_t off = static_cast<uint64_t>((k / 4) * (kPanelBytes >> 4) + (k % 4) * 2);
             mma_ss(tmem + kColS, qd + off, kd + off, idesc, k != 0 ? 1u : 0u);
           }
-          commit_elected(&s_full[i]);
-          if (j == w.n - 1) commit_elected(&q_empty[qi]);
-          if (i == i1 - 1) commit_elected(&kv_empty[ring.stage]);
+          tc_commit(&s_full[i]);
+          if (j == w.n - 1) tc_commit(&q_empty[qi]);
+          if (i == i1 - 1) tc_commit(&kv_empty[ring.stage]);
         }
         if (!ok) fault = kFaultMmaWait;
       }
     }
     if (fault != 0u) *abort_flag = 1;
     // every tcgen05 operation issued must complete before TMEM is released
-    commit_elected(&drain[0]);
+    tc_commit(&drain[0]);
     if (!mbar_wait(&drain[0], 0u, nullptr)) fault |= kFaultDrainWait;
     __syncwarp();
   } else if (warp == 10) {
@@ -431,14 +423,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           } else {
             for (int k = 0; k < k16; ++k) mma_ts(o, a + k * 8, vd + k * (2048 >> 4), idesc, (adds || k != 0) ? 1u : 0u);
           }
-          commit_elected(&pv_done[i]);
-          if (i == i1 - 1) commit_elected(&kv_empty[ring.v_stage()]);
+          tc_commit(&pv_done[i]);
+          if (i == i1 - 1) tc_commit(&kv_empty[ring.v_stage()]);
         }
         if (!ok) fault = kFaultMmaWait;
       }
     }
     if (fault != 0u) *abort_flag = 1;
-    commit_elected(&drain[1]);
+    tc_commit(&drain[1]);
     if (!mbar_wait(&drain[1], 0u, nullptr)) fault |= kFaultDrainWait;
     __syncwarp();
   } else if (warp < 8) {

@@ -25,8 +25,8 @@
 //         instruction holds its issuing thread long enough that one thread
 //         cannot keep the SM's TMA unit busy; two issuing warps reach about
 //         twice the load rate.
-//   1     allocates TMEM; in the leader one thread waits for one barrier per
-//         k-tile, issues the MMAs and commits once: that commit frees the
+//   1     allocates TMEM; in the leader the warp waits for one barrier per
+//         k-tile, issues the MMAs and commits once (by one elected lane): that commit frees the
 //         shared-memory stage and the TMEM scale slot of the k-tile together.
 //   2-5   epilogue: tcgen05.ld 32 columns at a time, alpha*acc + bias, bf16,
 //         swizzled staging in shared memory, TMA store (or the fused
@@ -361,7 +361,14 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16, kMx4>::kT
   };
   auto run_mma = [&]() {
     // ------------------------------------------------------------ MMA issuer (group leader)
-    if (lane == 0 && leader) {
+    if (leader) {
+      // a barrier wait of the whole warp (it issues the MMAs together, by its
+      // elected lane)
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = mbar_wait(bar, parity, abort_flag);
+        __syncwarp();
+        return __all_sync(0xffffffffu, ok) != 0;
+      };
       // one MMA k-block: NVFP4 reads 4 scale columns per k-block, MXFP4 two
       // bytes of 4 columns per two k-blocks; MXFP8 reads byte kb of the k-tile's scale words (named in the descriptor and in
       // the top two bits of the scale addresses)
@@ -409,14 +416,14 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16, kMx4>::kT
       int acc = 0;
       uint32_t acc_phase = 0;
       for (int tile = cluster; tile < p.num_tiles && fault == 0u; tile += num_clusters) {
-        if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u, abort_flag)) {
+        if (!wait(&acc_empty[acc], acc_phase ^ 1u)) {
           fault = kFaultMmaWait;
           break;
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kBN);
         for (int kt = kt_begin; kt < kt_end; ++kt) {
-          if (!mbar_wait(&full[stage], phase, abort_flag)) {
+          if (!wait(&full[stage], phase)) {
             fault = kFaultMmaWait;
             break;
           }
@@ -426,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16, kMx4>::kT
           const uint32_t sb = smem_u32(smem + C::kOffB + stage * C::kBBytes);
           const uint32_t sfa = tmem_base + C::kSfaCol + static_cast<uint32_t>(slot) * C::kSfaSlotCols;
           const uint32_t sfb = tmem_base + C::kSfbCol + static_cast<uint32_t>(slot) * C::kSfbSlotCols;
-          // One thread issues the MMAs and the tensor pipe queues few of them,
+          // One lane issues the MMAs and the tensor pipe queues few of them,
           // so the instructions between two MMAs are on the critical path: the
           // full k-tile takes a straight-line path with every operand address
           // formed up front (a descriptor's start address field counts 16-byte

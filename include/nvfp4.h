@@ -505,7 +505,8 @@ nvfp4_status nvfp4_rope(const nvfp4_rope_tensor* tensors, int32_t n_tensors,
  *   kv_lens    device array [batch] of valid states (clamped into
  *              [0, kv_tokens]), read when the kernel runs, or NULL for all.
  *              What k and v hold from there on does not matter, NaN included;
- *              an entry without states gets zeros.
+ *              an entry without states gets zeros (as do queries whose scores
+ *              are all -inf).
  *   scale      positive and finite (1 / sqrt(head_dim) as a rule)
  * Every extent >= 1; head_dim a multiple of 8, at most 128; q_heads a multiple
  * of kv_heads, at most 128 of them to a K/V head; out overlaps no input.  The

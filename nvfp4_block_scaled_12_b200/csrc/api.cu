@@ -608,7 +608,8 @@ nvfp4_status nvfp4_attention(const nvfp4_heads* q, const nvfp4_heads* k, const n
   p.tile_rows = p.tile_tokens * p.group;
   p.q_tiles = (p.q_tokens + p.tile_tokens - 1) / p.tile_tokens;
   p.pairs = (p.q_tiles + 1) / 2;
-  if (batch * kv_heads > INT32_MAX / p.pairs) return fail(NVFP4_EINVAL, "problem too large");
+  // (half of int32: an item's index plus a grid's worth of CTAs stays inside)
+  if (batch * kv_heads > INT32_MAX / 2 / p.pairs) return fail(NVFP4_EINVAL, "problem too large");
   p.items = static_cast<int32_t>(batch * kv_heads * p.pairs);
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   const DeviceInfo* dev = nullptr;

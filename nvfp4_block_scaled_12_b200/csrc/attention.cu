@@ -29,9 +29,9 @@
 // ring of K and V tiles, and a panel of O per slot on its way out.
 //
 // The reference m of a row is its first tile's maximum and moves only when a
-// later tile's sum of P exceeds what the type of P holds with room to spare
-// (2^15 in fp16, 2^60 in bf16; a relative accuracy is all that matters below):
-// then the tile is made again with its own maximum, and O is rescaled in TMEM.
+// later tile's sum of P exceeds 2^15 (fp16 holds that, and a relative accuracy
+// is all that matters below): then the tile is made again with its own maximum,
+// and O is rescaled in TMEM.
 // So only the first tile's maxima are ever taken; P of the others is made at
 // once, and the sum, which is needed anyway, is the check.  S, the maximum, the
 // sum and O are fp32; P is rounded to the type of V for the tensor cores (the
@@ -218,9 +218,13 @@ __device__ __forceinline__ AttItem att_item(const AttentionParams& p, int item, 
   w.slots = min(2, p.q_tiles - w.tile0);
   w.shared = p.join != 0 && p.q_tiles == 1;
   w.len = p.kv_lens != nullptr ? min(max(__ldg(p.kv_lens + w.b), 0), p.kv_tokens) : p.kv_tokens;
-  const int tiles = (w.len + kAttTile - 1) / kAttTile;
-  w.kt0 = static_cast<int>(static_cast<int64_t>(tiles) * rank / p.split);
-  w.n = static_cast<int>(static_cast<int64_t>(tiles) * (rank + 1) / p.split) - w.kt0;
+  const unsigned tiles = (static_cast<unsigned>(w.len) + kAttTile - 1) / kAttTile;  // (at most 2^23)
+  w.kt0 = 0;
+  w.n = static_cast<int>(tiles);
+  if (p.split > 1) {
+    w.kt0 = static_cast<int>(tiles * rank / p.split);
+    w.n = static_cast<int>(tiles * (rank + 1) / p.split) - w.kt0;
+  }
   return w;
 }
 
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                      const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_o,
                      const __grid_constant__ AttentionParams p) {
   using C = ACfg<kDP>;
-  constexpr float kMostSum = kFp16 ? 0x1p15f : 0x1p60f;
+  constexpr float kMostSum = 0x1p15f;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -506,8 +510,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         };
         // P of the keys from 64 h on with the present reference, two to a word
         uint32_t pk[32];
-        auto make_p = [&](int h) {
-          const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-m_ref * c, -m_ref * c);
+        auto make_p = [&](int h, float m) {
+          const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-m * c, -m * c);
           uint64_t sum[2] = {0u, 0u};
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
@@ -528,8 +532,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           tmem_st_32x32b_x16(t_p + 32 * h, *reinterpret_cast<const uint32_t(*)[16]>(pk));
           tmem_st_32x32b_x16(t_p + 32 * h + 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16));
         };
-        if (j == j0) m_ref = row_max();
-        float tile_sum = make_p(0);
+        // (a row without a finite score so far takes its next tile's maximum)
+        if (j == j0 || m_ref == -INFINITY) m_ref = row_max();
+        const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
+        float tile_sum = make_p(0, m_use);
         if (j > j0) {
           // the last tile's product has read P (and O is complete up to it)
           if (!all_lanes(mbar_wait(&pv_done[i], pv_phase, abort_flag))) {
@@ -540,15 +546,15 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           tc_fence_after();
         }
         store_p(0);
-        tile_sum += make_p(1);
+        tile_sum += make_p(1, m_use);
         if (j > j0) {
           const bool moves = tile_sum > kMostSum;
           if (__any_sync(0xffffffffu, moves)) {
             // rare: the tile's maximum becomes the reference, O and the sum so
             // far are scaled down to it, and P is made again
-            const float m_new = moves ? row_max() : m_ref;
-            const float f = moves ? exp2_approx((m_ref - m_new) * c) : 1.0f;
-            m_ref = m_new;
+            const float m_new = moves ? row_max() : m_use;
+            const float f = moves ? exp2_approx((m_use - m_new) * c) : 1.0f;
+            if (moves) m_ref = m_new;
             l_sum *= f;
 #pragma unroll 1
             for (int d = 0; d < kDP; d += 16) {
@@ -560,9 +566,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
               tmem_st_32x32b_x16(t_o + d, o);
             }
             tmem_st_wait();
-            tile_sum = make_p(0);
+            tile_sum = make_p(0, m_new);
             store_p(0);
-            tile_sum += make_p(1);
+            tile_sum += make_p(1, m_new);
           }
         }
         store_p(1);
@@ -585,7 +591,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       // ---- O / sum through shared memory, 64 columns at a time, to the output
       // (zeros where there are no states).  One row a thread straight to global
       // memory took 4200 clocks a tile: every store touched 32 lines.
-      const float inv = have ? 1.0f / l_sum : 0.0f;
+      const float inv = have && l_sum != 0.0f ? 1.0f / l_sum : 0.0f;
       uint8_t* panel = smem + C::kOffOut + i * kPanelBytes;
 #pragma unroll 1
       for (int d = 0; d < p.D; d += 64) {

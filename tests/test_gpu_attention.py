@@ -128,6 +128,28 @@ def test_one_key_takes_everything_bit_exact(F, dtype, D, Lq, Lk):
     assert torch.equal(o[0], v[0, pick])
 
 
+@pytest.mark.parametrize("Lq,Lk,inf_to", [(1, 600, 400), (200, 600, 400), (200, 300, 130), (1, 300, 300), (200, 300, 300)])
+def test_scores_of_minus_infinity(F, Lq, Lk, inf_to):
+    # a valid state whose key holds -inf (and queries that are positive there) has a probability of zero; the first
+    # tiles have nothing else, and the last two cases no finite score at all
+    q, k, v = (_rand((1, n, 4, 64), BF, 40 + n) for n in (Lq, Lk, Lk))
+    q[..., 0] = 1.0
+    k[:, :inf_to, :, 0] = float("-inf")
+    o = F.cross_attention(q, k, v)
+    if inf_to == Lk:
+        assert bool((o == 0).all())
+    else:
+        _check(o, q, k[:, inf_to:], v[:, inf_to:])
+
+
+def test_a_score_that_is_not_a_number_shows(F):
+    for Lq in (1, 200):
+        q, k, v = (_rand((1, n, 4, 64), BF, 50 + n) for n in (Lq, 600, 600))
+        k[0, 300, 1, 5] = float("nan")
+        o = F.cross_attention(q, k, v)
+        assert bool(torch.isnan(o[:, :, 1]).all()) and not bool(torch.isnan(o[:, :, [0, 2, 3]]).any())
+
+
 def test_equal_scores_give_the_mean(F):
     q = torch.zeros(2, 50, 2, 128, device="cuda", dtype=BF)
     k, v = _rand((2, 512, 2, 128), BF, 9), torch.ones(2, 512, 2, 128, device="cuda", dtype=BF)

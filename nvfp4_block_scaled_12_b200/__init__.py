@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -92,10 +93,9 @@ def _load() -> ctypes.CDLL:
     lib.nvfp4_mxfp4_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, f32, vp, vp, vp]
     lib.nvfp4_fp8row_quantize.argtypes = [vp, i64, i64, vp, vp, vp]
     lib.nvfp4_fp8row_gemm.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp, vp]
-    lib.nvfp4_rope.argtypes = [ctypes.POINTER(RopeTensor), i32, i64, i64, i64, i32, vp, i32, i64, i32,
-                               ctypes.POINTER(ctypes.c_int32), ctypes.c_double, i32, f32, vp]
-    hp = ctypes.POINTER(Heads)
-    lib.nvfp4_attention.argtypes = [hp, hp, hp, hp, i64, i64, i64, i64, i64, i64, i32, vp, f32, vp]
+    # (structures by address: the helpers pass their bytes)
+    lib.nvfp4_rope.argtypes = [vp, i32, i64, i64, i64, i32, vp, i32, i64, i32, vp, ctypes.c_double, i32, f32, vp]
+    lib.nvfp4_attention.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i32, vp, f32, vp]
     lib.nvfp4_dequantize.argtypes = [vp, vp, f32, i64, i64, vp, vp]
     lib.nvfp4_w4a16_gemm.argtypes = [vp, vp, vp, i64, i64, i64, f32, vp, vp, vp]
     lib.nvfp4_check_fault.argtypes = []
@@ -243,20 +243,32 @@ def nvfp4_fp8row_gemm(a: int, a_scale: int, b: int, b_scale: int, M: int, N: int
     _check(library().nvfp4_fp8row_gemm(a, a_scale, b, b_scale, M, N, K, bias or None, y, stream))
 
 
-def nvfp4_rope(tensors: Sequence[RopeTensor], batch: int, tokens: int, head_dim: int, dtype: int, positions: int,
-               pos_type: int, pos_batch_stride: int, axis_dims: Sequence[int], theta: float, flags: int, eps: float,
+_HEADS = struct.Struct("@P3q")          # nvfp4_heads
+_ROPE_TENSOR = struct.Struct("@P3qP3qqP")  # nvfp4_rope_tensor
+
+
+def _address(x):
+    """A structure as a pointer argument: itself by reference, or its bytes."""
+    return x if type(x) is bytes else ctypes.byref(x)
+
+
+def nvfp4_rope(tensors, batch: int, tokens: int, head_dim: int, dtype: int, positions: int, pos_type: int,
+               pos_batch_stride: int, axis_dims: Sequence[int], theta: float, flags: int, eps: float,
                stream: int) -> None:
-    arr = (RopeTensor * len(tensors))(*tensors)
-    dims = (ctypes.c_int32 * len(axis_dims))(*axis_dims)
-    _check(library().nvfp4_rope(arr, len(tensors), batch, tokens, head_dim, dtype, positions, pos_type,
-                                pos_batch_stride, len(axis_dims), dims, theta, flags, eps, stream))
+    """``tensors`` is a sequence of RopeTensor, or the bytes of one or two."""
+    if type(tensors) is not bytes:
+        tensors = b"".join(bytes(t) for t in tensors)
+    n = len(axis_dims)
+    _check(library().nvfp4_rope(tensors, len(tensors) // _ROPE_TENSOR.size, batch, tokens, head_dim, dtype, positions,
+                                pos_type, pos_batch_stride, n, struct.pack(f"@{n}i", *axis_dims), theta, flags, eps,
+                                stream))
 
 
-def nvfp4_attention(q: Heads, k: Heads, v: Heads, out: Heads, batch: int, q_tokens: int, kv_tokens: int,
-                    q_heads: int, kv_heads: int, head_dim: int, dtype: int, kv_lens: int, scale: float,
-                    stream: int) -> None:
-    _check(library().nvfp4_attention(q, k, v, out, batch, q_tokens, kv_tokens, q_heads, kv_heads, head_dim, dtype,
-                                     kv_lens or None, scale, stream))
+def nvfp4_attention(q, k, v, out, batch: int, q_tokens: int, kv_tokens: int, q_heads: int, kv_heads: int,
+                    head_dim: int, dtype: int, kv_lens: int, scale: float, stream: int) -> None:
+    """``q``, ``k``, ``v`` and ``out`` are Heads, or their bytes."""
+    _check(library().nvfp4_attention(_address(q), _address(k), _address(v), _address(out), batch, q_tokens, kv_tokens,
+                                     q_heads, kv_heads, head_dim, dtype, kv_lens or None, scale, stream))
 
 
 def nvfp4_dequantize(codes: int, sf: int, g: float, rows: int, K: int, out: int, stream: int) -> None:
@@ -682,13 +694,23 @@ def _need_heads(t, name, dev, dtype=None, shape=None):
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _heads(t) -> Heads:
+def _heads(t) -> bytes:
+    """``t`` [batch, tokens, heads, head_dim] as the bytes of an nvfp4_heads."""
     sb, st, sh, _ = t.stride()
-    return Heads(t.data_ptr(), sb, st, sh)
+    return _HEADS.pack(t.data_ptr(), sb, st, sh)
 
 
-def _empty_on(stream, shape, like, dtype=None):
-    """A new tensor on ``like``'s device (of its type, or ``dtype``), owned by the stream that writes it."""
+def _like(stream, t):
+    """A contiguous new tensor of ``t``'s shape and type, owned by the stream that writes it."""
+    torch = _torch_module or _torch()
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _empty_on(stream, shape, like, dtype):
+    """A new tensor of ``dtype`` on ``like``'s device, owned by the stream that writes it."""
     if stream is None:
         return like.new_empty(shape, dtype=dtype)
     with _torch().cuda.stream(stream):
@@ -712,33 +734,37 @@ def rope(q, positions, axes: Sequence[int], k=None, theta: float = 10000.0, q_we
     dev = torch.cuda.current_device()
     _need_heads(q, "q", dev)
     B, L, _, D = q.shape
-    if k is None and (k_weight is not None or k_out is not None):
-        raise ValueError("k_weight and k_out need k")
-    results, args = [], []
-    for name, x, weight, out in (("q", q, q_weight, q_out), ("k", k, k_weight, k_out)):
-        if x is None:
-            continue
-        if name == "k":
-            _need_heads(x, name, dev, q.dtype, (B, L, x.shape[2] if x.dim() == 4 else 0, D))
-        if weight is not None:
-            _need(weight, q.dtype, (D,), f"{name}_weight", dev=dev)
-        if out is None:
-            out = _empty_on(stream, x.shape, x)
-        else:
-            _need_heads(out, f"{name}_out", dev, q.dtype, x.shape)
-        results.append(out)
-        args.append(RopeTensor(_heads(x), _heads(out), x.shape[2], _ptr(weight)))
+    dtype, n = q.dtype, len(axes)
     if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.float32):
         raise TypeError("positions must be an int32 or float32 CUDA tensor")
-    n = len(axes)
-    if tuple(positions.shape) not in ((L, n), (B, L, n)):
+    if positions.shape != (L, n) and positions.shape != (B, L, n):
         raise ValueError(f"positions must be [{L}, {n}] or [{B}, {L}, {n}], got {tuple(positions.shape)}")
     _need(positions, positions.dtype, None, "positions", dev=dev)
-    nvfp4_rope(args, B, L, D, DTYPE_FP16 if q.dtype == torch.float16 else DTYPE_BF16, _ptr(positions),
+
+    def tensor(x, name, weight, out):
+        if weight is not None:
+            _need(weight, dtype, (D,), f"{name}_weight", dev=dev)
+        if out is None:
+            out = _like(stream, x)
+        else:
+            _need_heads(out, f"{name}_out", dev, dtype, x.shape)
+        ib, it, ih, _ = x.stride()
+        ob, ot, oh, _ = out.stride()
+        return out, _ROPE_TENSOR.pack(x.data_ptr(), ib, it, ih, out.data_ptr(), ob, ot, oh, x.shape[2], _ptr(weight))
+
+    if k is not None:
+        _need_heads(k, "k", dev, dtype, (B, L, k.shape[2] if k.dim() == 4 else 0, D))
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
+    q_out, tensors = tensor(q, "q", q_weight, q_out)
+    if k is not None:
+        k_out, k_tensor = tensor(k, "k", k_weight, k_out)
+        tensors += k_tensor
+    nvfp4_rope(tensors, B, L, D, DTYPE_FP16 if dtype == torch.float16 else DTYPE_BF16, positions.data_ptr(),
                POS_FLOAT32 if positions.dtype == torch.float32 else POS_INT32, L * n if positions.dim() == 3 else 0,
                axes, float(theta), ROPE_INTERLEAVED * bool(interleaved) + ROPE_SHARED_LADDER * bool(shared),
                float(eps), _stream(stream))
-    return results[0] if k is None else tuple(results)
+    return q_out if k is None else (q_out, k_out)
 
 
 def cross_attention(q, k, v, kv_lens=None, scale: Optional[float] = None, out=None, stream=None):
@@ -761,7 +787,7 @@ def cross_attention(q, k, v, kv_lens=None, scale: Optional[float] = None, out=No
     if kv_lens is not None:
         _need(kv_lens, torch.int32, (B,), "kv_lens", dev=dev)
     if out is None:
-        out = _empty_on(stream, q.shape, q)
+        out = _like(stream, q)
     else:
         _need_heads(out, "out", dev, q.dtype, q.shape)
     nvfp4_attention(_heads(q), _heads(k), _heads(v), _heads(out), B, Lq, k.shape[1], Hq, k.shape[2], D,

@@ -577,7 +577,8 @@ nvfp4_status nvfp4_attention(const nvfp4_heads* q, const nvfp4_heads* k, const n
     return fail(NVFP4_EINVAL, "q_heads=%lld must be a multiple of kv_heads=%lld, at most 128 to each",
                 (long long)q_heads, (long long)kv_heads);
   if (dtype != NVFP4_DTYPE_BF16 && dtype != NVFP4_DTYPE_FP16) return fail(NVFP4_EINVAL, "unknown dtype %d", dtype);
-  if (!finite_f(scale) || scale <= 0.0f) return fail(NVFP4_EINVAL, "scale must be positive and finite");
+  const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);  // times log2 e
+  if (!finite_f(scale_log2) || scale <= 0.0f) return fail(NVFP4_EINVAL, "scale must be positive and finite");
   if (reinterpret_cast<uintptr_t>(kv_lens) % 4 != 0) return fail(NVFP4_EALIGN, "kv_lens must be 4-byte aligned");
   const struct {
     const char* name;
@@ -611,7 +612,7 @@ nvfp4_status nvfp4_attention(const nvfp4_heads* q, const nvfp4_heads* k, const n
   // (half of int32: an item's index plus a grid's worth of CTAs stays inside)
   if (batch * kv_heads > INT32_MAX / 2 / p.pairs) return fail(NVFP4_EINVAL, "problem too large");
   p.items = static_cast<int32_t>(batch * kv_heads * p.pairs);
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.scale_log2 = scale_log2;
   const DeviceInfo* dev = nullptr;
   st = current_device(&dev);
   if (st != NVFP4_OK) return st;

@@ -68,8 +68,9 @@ struct ACfg {
   static constexpr uint32_t kOffKv = 2 * kTileBytes;
   static constexpr uint32_t kOffOut = kOffKv + kStages * kTileBytes;  // a panel of O on its way out, per slot
   static constexpr uint32_t kOffBar = kOffOut + 2 * kPanelBytes;
-  // kv_full, kv_empty per stage; q_full, q_empty, s_full, p_ready, pv_done per slot; s_free, two drains
-  static constexpr uint32_t kNumBars = 2 * kStages + 10 + 3;
+  // kv_full, kv_empty per stage; q_full, q_empty, s_full, p_ready, pv_done, o_free,
+  // o_written, drain per slot; s_free
+  static constexpr uint32_t kNumBars = 2 * kStages + 16 + 1;
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
   static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;  // + alignment slack
   // K/V split: a slot's fp32 partial rows (padded to spread them over the
@@ -245,8 +246,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   uint64_t* s_full = q_empty + 2;
   uint64_t* p_ready = s_full + 2;
   uint64_t* pv_done = p_ready + 2;
-  uint64_t* s_free = pv_done + 2;
-  uint64_t* drain = s_free + 1;
+  uint64_t* o_free = pv_done + 2;
+  uint64_t* o_written = o_free + 2;
+  uint64_t* drain = o_written + 2;
+  uint64_t* s_free = drain + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const int warp = threadIdx.x >> 5;
@@ -266,9 +269,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], 4);  // the slot's four softmax warps
       mbar_init(&pv_done[i], 1);
+      mbar_init(&o_free[i], 1);
+      mbar_init(&o_written[i], 4);  // the slot's four softmax warps
+      mbar_init(&drain[i], 1);
     }
     mbar_init(s_free, 4);  // the four softmax warps that read S
-    for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -449,7 +454,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const uint32_t t_s = tmem + kColS + t_lane, t_p = tmem + kColP + i * kSlotP + t_lane;
     const uint32_t t_o = tmem + kColO + i * kSlotO + t_lane;
     const float c = p.scale_log2;
-    uint32_t s_phase = 0u, pv_phase = 0u;
+    uint32_t s_phase = 0u, pv_phase = 0u, o_phase = 0u;
     RingPos<S> ring;  // of this step's K
     auto all_lanes = [&](bool ok) {
       __syncwarp();
@@ -595,8 +600,16 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       uint8_t* panel = smem + C::kOffOut + i * kPanelBytes;
 #pragma unroll 1
       for (int d = 0; d < p.D; d += 64) {
-        if (row == 0) bulk_wait_read<0>();  // the last panel has left
-        named_barrier_sync(2 + i, 128);
+        // (barriers with bounded waits between the slot's warps: after a
+        // fault one of them may be gone)
+        if (row == 0) {
+          bulk_wait_read<0>();  // the last panel has left
+          mbar_arrive(&o_free[i]);
+        }
+        if (!all_lanes(mbar_wait(&o_free[i], o_phase, abort_flag))) {
+          fault = kFaultEpilogueWait;
+          break;
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t o[32];
@@ -617,11 +630,19 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           }
         }
         fence_async_smem();
-        named_barrier_sync(2 + i, 128);
-        if (row == 0) {  // (rows past the queries and columns past the width are clipped)
-          tma_store_4d(&tmap_o, panel, d, w.hk * p.group, (w.tile0 + i) * p.tile_tokens, w.b);
-          bulk_commit();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_written[i]);
+        if ((warp & 3) == 0) {
+          if (!all_lanes(mbar_wait(&o_written[i], o_phase, abort_flag))) {
+            fault = kFaultEpilogueWait;
+            break;
+          }
+          if (lane == 0) {  // (rows past the queries and columns past the width are clipped)
+            tma_store_4d(&tmap_o, panel, d, w.hk * p.group, (w.tile0 + i) * p.tile_tokens, w.b);
+            bulk_commit();
+          }
         }
+        o_phase ^= 1u;
       }
       tc_fence_before();  // these reads of O come before the next item's P V
     }

@@ -1,6 +1,8 @@
 """Argument checks of the entry points on 16-bit heads, on the CPU: the C ABI
 refuses before it touches a device, the torch helpers before they hand a
 pointer on."""
+import ctypes
+
 import pytest
 import torch
 
@@ -65,7 +67,10 @@ def test_rope_helper(calls):
     assert got[0] is qo and got[1] is ko
     assert F.rope(q, empty(2, 9, 2, dtype=torch.float32), [32, 32], q_out=q) is q
     (_, a), (_, b) = calls
-    assert len(a[0]) == 2 and a[0][0].norm_weight and not a[0][1].norm_weight and a[0][1].heads == 2
+    first, second = (F.RopeTensor.from_buffer_copy(a[0], i * len(a[0]) // 2) for i in range(2))
+    assert len(a[0]) == 2 * ctypes.sizeof(F.RopeTensor) and first.norm_weight and not second.norm_weight
+    assert (first.heads, second.heads) == (4, 2) and first.in_.data == q.data_ptr() and second.out.data == ko.data_ptr()
+    assert (first.in_.batch_stride, first.in_.token_stride, first.in_.head_stride) == (9 * 256, 256, 64)
     assert a[1:5] == (2, 9, 64, 0) and a[6] == F.POS_INT32 and a[7] == 0 and b[6] == F.POS_FLOAT32 and b[7] == 18
     wide = empty(2, 9, 4, 128, dtype=BF)
     for bad in (lambda: F.rope(empty(2, 9, 4, 64, dtype=torch.float32), pos, [32, 32], q_out=qo),
@@ -102,7 +107,7 @@ def attention_args(**kw):
     dict(batch=0), dict(q_tokens=0), dict(kv_tokens=0), dict(q_heads=0), dict(kv_heads=0), dict(head_dim=0),
     dict(head_dim=68), dict(head_dim=136), dict(q_heads=8, kv_heads=3), dict(q_heads=258, kv_heads=2, batch=1),
     dict(dtype=2), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
-    dict(batch=1 << 29, kv_heads=8), dict(q=heads(data=0)), dict(out=heads(data=0)), dict(k=heads(token=4)),
+    dict(scale=3e38), dict(batch=1 << 29, kv_heads=8), dict(q=heads(data=0)), dict(out=heads(data=0)), dict(k=heads(token=4)),
     dict(v=heads(head=-64)), dict(k=heads(token=0)), dict(q=heads(head=0)), dict(out=heads(batch=0)),
     dict(out=heads(head=56)), dict(k=heads(batch=1 << 40))])
 def test_attention_rejects_bad_arguments(kw):

@@ -364,8 +364,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     RingPos<S> ring;  // of the present step's K
     uint32_t q_phase[2] = {0u, 0u}, s_phase = 1u;  // (nobody has S at the start)
     auto wait = [&](uint64_t* bar, uint32_t parity) {  // of the whole warp
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
       const bool ok = mbar_wait(bar, parity, abort_flag);
-      __syncwarp();
       return __all_sync(0xffffffffu, ok) != 0;
     };
     for (int item = first; item < p.items && fault == 0u; item += step) {
@@ -408,8 +408,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     RingPos<S> ring;
     uint32_t p_phase[2] = {0u, 0u};
     auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
       const bool ok = mbar_wait(bar, parity, abort_flag);
-      __syncwarp();
       return __all_sync(0xffffffffu, ok) != 0;
     };
     for (int item = first; item < p.items && fault == 0u; item += step) {
@@ -460,6 +460,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       __syncwarp();
       return __all_sync(0xffffffffu, ok) != 0;
     };
+    // a barrier wait of the whole warp (its first try by itself, as cheap as can be)
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+      return all_lanes(mbar_wait(bar, parity, abort_flag));
+    };
     for (int item = first; item < p.items && fault == 0u; item += step) {
       const AttItem w = att_item(p, item, rank);
       if (i >= w.slots && !w.shared) {
@@ -473,7 +478,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       for (int j = 0; j < w.n; ++j, ring.next_step()) {
         if (w.shared && (j & 1) != i) continue;
         const int valid = w.len - (w.kt0 + j) * kAttTile;  // keys of this tile (more than 128: all)
-        if (!all_lanes(mbar_wait(&s_full[i], s_phase, abort_flag))) {
+        if (!wait_all(&s_full[i], s_phase)) {
           fault = kFaultEpilogueWait;
           break;
         }
@@ -494,7 +499,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           if ((i == 0 || w.shared) && (valid & 15) != 0) {
             // the V rows from the last valid state to the next multiple of 16
             // keys: zero, whatever they hold (0 * NaN would not be)
-            if (!all_lanes(mbar_wait(&kv_full[ring.v_stage()], ring.v_phase(), abort_flag))) {
+            if (!wait_all(&kv_full[ring.v_stage()], ring.v_phase())) {
               fault = kFaultEpilogueWait;
               break;
             }
@@ -543,7 +548,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         float tile_sum = make_p(0, m_use);
         if (j > j0) {
           // the last tile's product has read P (and O is complete up to it)
-          if (!all_lanes(mbar_wait(&pv_done[i], pv_phase, abort_flag))) {
+          if (!wait_all(&pv_done[i], pv_phase)) {
             fault = kFaultEpilogueWait;
             break;
           }
@@ -585,7 +590,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
       }
       if (fault != 0u) break;
       if (have) {
-        if (!all_lanes(mbar_wait(&pv_done[i], pv_phase, abort_flag))) {
+        if (!wait_all(&pv_done[i], pv_phase)) {
           fault = kFaultEpilogueWait;
           break;
         }
@@ -606,7 +611,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           bulk_wait_read<0>();  // the last panel has left
           mbar_arrive(&o_free[i]);
         }
-        if (!all_lanes(mbar_wait(&o_free[i], o_phase, abort_flag))) {
+        if (!wait_all(&o_free[i], o_phase)) {
           fault = kFaultEpilogueWait;
           break;
         }
@@ -633,7 +638,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&o_written[i]);
         if ((warp & 3) == 0) {
-          if (!all_lanes(mbar_wait(&o_written[i], o_phase, abort_flag))) {
+          if (!wait_all(&o_written[i], o_phase)) {
             fault = kFaultEpilogueWait;
             break;
           }

@@ -365,8 +365,9 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16, kMx4>::kT
       // a barrier wait of the whole warp (it issues the MMAs together, by its
       // elected lane)
       auto wait = [&](uint64_t* bar, uint32_t parity) {
+        // (the first try by itself: what stands between two k-tiles counts)
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
         const bool ok = mbar_wait(bar, parity, abort_flag);
-        __syncwarp();
         return __all_sync(0xffffffffu, ok) != 0;
       };
       // one MMA k-block: NVFP4 reads 4 scale columns per k-block, MXFP4 two

@@ -86,3 +86,70 @@ def test_attention_block(F, B, L, Lk, heads, D):
     replayed = captured.clone()
     assert torch.equal(replayed, run())
     F.nvfp4_check_fault()
+
+
+def _calls(F, seed):
+    """The operators on inputs of their own, at sizes that take clusters, pairs and one-CTA tiles, and their results
+    when nothing else runs."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device="cuda").bfloat16()
+
+    q, k, v = rand(2, 5, 8, 128), rand(2, 3000, 4, 128), rand(2, 3000, 4, 128)
+    lens = torch.tensor([3000, 1234], dtype=torch.int32).cuda()
+    big = rand(1, 900, 12, 64), rand(1, 300, 12, 64), rand(1, 300, 12, 64)
+    pos = torch.randint(0, 99, (900, 2), dtype=torch.int32).cuda()
+    weights = [F.quantize_mxfp4(rand(n, 448)) for n in (520, 1024)]
+    xs = [rand(m, 448) for m in (1, 300, 3000)]
+
+    def run():
+        out = [F.cross_attention(q, k, v, kv_lens=lens), F.cross_attention(*big), F.rope(big[0], pos, [32, 32])]
+        for x in xs:
+            for w in weights:
+                out.append(F.gemm_mxfp4(F.quantize_mxfp4(x), w))
+        return out
+
+    return run
+
+
+def test_streams_and_host_threads_at_once(F):
+    from concurrent.futures import ThreadPoolExecutor
+    runs = [_calls(F, seed) for seed in range(4)]
+    want = [run() for run in runs]
+    torch.cuda.synchronize()
+
+    def worker(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            got = [runs[i]() for _ in range(5)]
+        stream.synchronize()
+        return got
+
+    with ThreadPoolExecutor(4) as pool:
+        for i, rounds in enumerate(pool.map(worker, range(4))):
+            for got in rounds:
+                for a, b in zip(got, want[i]):
+                    assert torch.equal(a, b)
+    F.nvfp4_check_fault()
+
+
+def test_outputs_given_nothing_is_allocated(F):
+    q, k = torch.randn(1, 40, 4, 64, device="cuda").half(), torch.randn(1, 2000, 2, 64, device="cuda").half()
+    x, w = torch.randn(70, 192, device="cuda").bfloat16(), F.quantize_mxfp4(torch.randn(64, 192, device="cuda").bfloat16())
+    pos = torch.zeros(40, 1, dtype=torch.int32, device="cuda")
+    xq, y, o = F.quantize_mxfp4(x), torch.empty(70, 64, dtype=torch.bfloat16, device="cuda"), torch.empty_like(q)
+
+    def run():
+        F.quantize_mxfp4(x, out=xq)
+        F.gemm_mxfp4(xq, w, y=y)
+        F.rope(q, pos, [64], q_out=o)
+        F.cross_attention(q, k, k, out=o)
+
+    run()
+    torch.cuda.synchronize()
+    before, free = torch.cuda.memory_stats()["allocation.all.allocated"], torch.cuda.mem_get_info()[0]
+    run()
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+    assert torch.cuda.mem_get_info()[0] == free

@@ -42,6 +42,18 @@
 // MMA reads beyond them (up to the next multiple of 16 keys) are zeroed in
 // shared memory, since 0 * NaN is NaN.  Keys past the tensor arrive as zeros.
 //
+// What bounds it: the tensor cores' floor is 2048 clocks a step (two slots, two
+// products), the exponentials' 2048 (16 a clock and SM); a step takes 3300.  The
+// softmax warps are busy for 2560 to 2930 of them: those that share a scheduler
+// with an MMA issuer are the slow ones.  Joint attention of 4608 tokens, 24 heads
+// of 128: 200 us back to back = 1.31 PFLOP/s (0.79 of the measured bf16 burst;
+// under the power cap 236); heads of 64: 180 us (113 are the exponentials' floor);
+// 4096 queries over 512 and 382 states, 24 heads of 128: 59.5 us, a quarter of it
+// between items; one query over 16384 states, 32 heads on 8, batch 4: 54 us.
+// Measured and not kept: a share of the exponentials as a cubic on the FMA pipes
+// (no gain at any share), two threads a row (a vote a tile: the same speed), an
+// output warpgroup of its own (206 us), P handed over in halves.
+//
 // With fewer items than SMs the keys are split over the CTAs of a cluster, and
 // where all queries of a K/V head fit one tile the two slots take its key tiles
 // in turn: each part keeps its own m, sum and O, and they are joined through

@@ -42,6 +42,11 @@
 //   0, 2 producers, 1 MMA issuer, 3 idle; 4-11 epilogue, two warps per lane
 //   quarter (one per 128-column half), each reading its whole 128-column
 //   slice into registers before releasing the accumulator; 12-15 movers.
+// MXFP4 (kMx4) differs in its scales alone: two atoms per 128-row block and
+// k-tile instead of four, so the movers have half the work: MLP-up (M = 4608,
+// N = 12288, K = 3072) 71.4 us = 4.87 PFLOP/s against NVFP4's 77.8 (0.74 and
+// 0.68 of four times the measured bf16 burst); bound, like NVFP4's, by the
+// MMA warp's wait per k-tile and the hand-off of the one accumulator.
 // TMEM columns: the accumulators first, then the scale slots: 16 columns of A
 // scales each (4 per MMA k-block), then kBN/8 columns of B scales each
 // (kBN/32 per k-block).  Scale column j of lane l holds the 4 scales of row

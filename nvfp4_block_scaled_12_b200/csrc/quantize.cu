@@ -17,6 +17,12 @@
 // bytes of codes, written as one whole 32-byte sector.  The consumers' work,
 // not HBM, set the pace with 16 warps; 24 keep more rows in flight.
 //
+// MXFP8 and MXFP4 (power-of-two scales of 32 elements, from the exponent bits of
+// the block's maximum) take the same tiles: a thread's 64 elements are two
+// blocks and half a scale word.  MXFP4 moves NVFP4's bytes less half the scales:
+// [4608,12288] 28.0 us back to back = 5.1 TB/s (0.79 of the measured copy),
+// [4608,3072] 10.4 us, like NVFP4's.
+//
 // The dynamic variant measures the per-tensor scale in the same launch: every
 // CTA first takes max |x| over its own tiles (plain 16-byte loads), folds it
 // into a grid-wide maximum and arrives on a grid-wide counter; the producer

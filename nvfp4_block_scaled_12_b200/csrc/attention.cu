@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           float l = 0.0f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
           for (int t = 0; t < p.split * per_rank; ++t) {
             const float2 x = ld_shared_cluster_f2(part_at(ml, 128 * 8, t));
-            if (x.x == -INFINITY) continue;  // no states in that range
+            if (x.y == 0.0f) continue;  // no states in that range, or no finite score (a NaN's sum is NaN)
             const float f = exp2_approx((x.x - m) * p.scale_log2);
             l = fmaf(x.y, f, l);
             const uint32_t at = part_at(src, C::kPartSlot, t);
@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             v[6] = fmaf(b.z, f, v[6]);
             v[7] = fmaf(b.w, f, v[7]);
           }
-          const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
           const int token = (w.tile0 + i) * p.tile_tokens + row / p.group;
           uint16_t* out = static_cast<uint16_t*>(p.out) + w.b * p.out_batch + static_cast<int64_t>(token) * p.out_token +
                           static_cast<int64_t>(w.hk * p.group + row % p.group) * p.out_head;

@@ -150,6 +150,16 @@ def test_a_score_that_is_not_a_number_shows(F):
         assert bool(torch.isnan(o[:, :, 1]).all()) and not bool(torch.isnan(o[:, :, [0, 2, 3]]).any())
 
 
+@pytest.mark.parametrize("Lq,Lk", [(1, 200), (1, 3000), (200, 600), (3000, 300)])
+def test_a_query_that_is_not_a_number_shows(F, Lq, Lk):
+    # (keys in one CTA's hands and split over several)
+    q, k, v = (_rand((1, n, 4, 64), BF, 60 + n) for n in (Lq, Lk, Lk))
+    q[0, Lq // 2, 1, 5] = float("nan")
+    bad = torch.zeros(1, Lq, 4, 64, dtype=torch.bool, device="cuda")
+    bad[0, Lq // 2, 1] = True
+    assert torch.equal(torch.isnan(F.cross_attention(q, k, v)), bad)
+
+
 def test_equal_scores_give_the_mean(F):
     q = torch.zeros(2, 50, 2, 128, device="cuda", dtype=BF)
     k, v = _rand((2, 512, 2, 128), BF, 9), torch.ones(2, 512, 2, 128, device="cuda", dtype=BF)

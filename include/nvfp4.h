@@ -454,8 +454,9 @@ typedef struct {
 enum { NVFP4_POS_INT32 = 0, NVFP4_POS_FLOAT32 = 1 };
 enum { NVFP4_ROPE_INTERLEAVED = 1, NVFP4_ROPE_SHARED_LADDER = 2 };
 
-/* One tensor to rotate.  out may be in itself (in place), or must not overlap
- * it.  norm_weight [head_dim] (of the tensor's type) or NULL: with it, each
+/* One tensor to rotate.  out may be in itself (in place, with in's strides), or
+ * must not overlap it; neither may overlap what the other tensor of the call
+ * writes.  No two elements of an out share an address.  norm_weight [head_dim] (of the tensor's type) or NULL: with it, each
  * head is first divided by its root mean square and multiplied by the weight. */
 typedef struct {
   nvfp4_heads in, out;
@@ -506,7 +507,7 @@ nvfp4_status nvfp4_rope(const nvfp4_rope_tensor* tensors, int32_t n_tensors,
  *              [0, kv_tokens]), read when the kernel runs, or NULL for all.
  *              What k and v hold from there on does not matter, NaN included;
  *              an entry without states gets zeros (as do queries whose scores
- *              are all -inf).
+ *              are all -inf); a NaN among a query's valid scores gives it NaN.
  *   scale      positive and finite (1 / sqrt(head_dim) as a rule)
  * Every extent >= 1; head_dim a multiple of 8, at most 128; q_heads a multiple
  * of kv_heads, at most 128 of them to a K/V head; out overlaps no input.  The

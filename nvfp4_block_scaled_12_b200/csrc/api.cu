@@ -273,7 +273,8 @@ nvfp4_status gemm_common(const uint8_t* a, const uint8_t* sfa, const uint8_t* b,
 }
 
 // Checks one heads tensor: extents are those of the call, strides those of
-// extents above one.  written: two elements may not share an address.
+// extents above one.  written: two elements may not share an address, that is,
+// each stride goes past all that the smaller ones reach.
 nvfp4_status check_heads(const char* name, const nvfp4_heads& t, int64_t batch, int64_t tokens, int64_t heads,
                          int64_t head_dim, bool written) {
   if (!t.data) return fail(NVFP4_EINVAL, "%s: null pointer", name);
@@ -284,11 +285,20 @@ nvfp4_status check_heads(const char* name, const nvfp4_heads& t, int64_t batch, 
     if (extent[i] == 1) continue;
     if (stride[i] < 0 || stride[i] % 8 != 0 || stride[i] > (int64_t(1) << 38))
       return fail(NVFP4_EINVAL, "%s: stride %lld must be a multiple of 8 in [0, 2^38]", name, (long long)stride[i]);
-    if (written && stride[i] < head_dim)
-      return fail(NVFP4_EINVAL, "%s: stride %lld lets two heads of %lld overlap", name, (long long)stride[i],
-                  (long long)head_dim);
   }
-  return NVFP4_OK;
+  if (!written) return NVFP4_OK;
+  __int128 reach = head_dim;  // elements from the first one to the last of the strides taken so far
+  bool taken[3] = {extent[0] == 1, extent[1] == 1, extent[2] == 1};
+  for (;;) {
+    int least = -1;
+    for (int i = 0; i < 3; ++i)
+      if (!taken[i] && (least < 0 || stride[i] < stride[least])) least = i;
+    if (least < 0) return NVFP4_OK;
+    if (stride[least] < reach)
+      return fail(NVFP4_EINVAL, "%s: stride %lld lets two heads overlap", name, (long long)stride[least]);
+    reach += static_cast<__int128>(extent[least] - 1) * stride[least];
+    taken[least] = true;
+  }
 }
 
 // Tensor map of a heads tensor, [head_dim, heads, tokens, batch] with boxes of
@@ -527,6 +537,11 @@ nvfp4_status nvfp4_rope(const nvfp4_rope_tensor* tensors, int32_t n_tensors, int
                         static_cast<int32_t>(t.heads),
                         0};
     norm |= t.norm_weight != nullptr;
+    const RopeTensor& r = p.t[i];
+    if (r.in == r.out && (r.in_batch != r.out_batch || r.in_token != r.out_token || r.in_head != r.out_head))
+      return fail(NVFP4_EINVAL, "out in place of in needs in's strides");
+    if (i == 1 && (r.out == p.t[0].out || r.out == p.t[0].in || r.in == p.t[0].out))
+      return fail(NVFP4_EINVAL, "the second tensor shares its data with what the first one writes, or writes the first's");
   }
   p.positions = positions;
   p.pos_batch_stride = pos_batch_stride;
@@ -593,6 +608,8 @@ nvfp4_status nvfp4_attention(const nvfp4_heads* q, const nvfp4_heads* k, const n
   }
   nvfp4_status st = check_heads("out", *out, batch, q_tokens, q_heads, head_dim, true);
   if (st != NVFP4_OK) return st;
+  if (out->data == q->data || out->data == k->data || out->data == v->data)
+    return fail(NVFP4_EINVAL, "out overlaps an input");
 
   AttentionParams p = {};
   p.out = out->data;

@@ -11,6 +11,7 @@ from tests.test_abi import P, _expect
 from tests.test_binding_checks import empty
 
 BF = torch.bfloat16
+Q, R = P + (1 << 24), P + (2 << 24)
 
 
 def heads(batch=64 * 512, token=512, head=64, data=P):
@@ -34,9 +35,18 @@ def rope_args(**kw):
     dict(tensors=[F.RopeTensor(heads(data=0), heads(), 8, 0)]),
     dict(tensors=[F.RopeTensor(heads(token=508), heads(), 8, 0)]),
     dict(tensors=[F.RopeTensor(heads(token=-512), heads(), 8, 0)]),
-    dict(tensors=[F.RopeTensor(heads(), heads(head=56), 8, 0)]),
-    dict(tensors=[F.RopeTensor(heads(), heads(batch=0), 8, 0)]),
-    dict(tensors=[F.RopeTensor(heads(), heads(), 8, 0)] * 3)])
+    dict(tensors=[F.RopeTensor(heads(), heads(head=56, data=Q), 8, 0)]),
+    dict(tensors=[F.RopeTensor(heads(), heads(batch=0, data=Q), 8, 0)]),
+    dict(tensors=[F.RopeTensor(heads(), heads(), 8, 0)] * 3),
+    # outputs that overlap themselves: tokens inside one another's heads, batches inside one another's tokens
+    dict(tensors=[F.RopeTensor(heads(), heads(token=64, data=Q), 8, 0)]),
+    dict(tensors=[F.RopeTensor(heads(), heads(batch=63 * 512, data=Q), 8, 0)]),
+    dict(tensors=[F.RopeTensor(heads(), heads(token=64, head=128, data=Q), 8, 0)]),
+    # in place with other strides; the second tensor's output as the first's, its input as the first's output
+    dict(tensors=[F.RopeTensor(heads(), heads(token=64, head=64 * 64), 8, 0)]),
+    dict(tensors=[F.RopeTensor(heads(), heads(data=Q), 8, 0), F.RopeTensor(heads(data=R), heads(data=Q), 8, 0)]),
+    dict(tensors=[F.RopeTensor(heads(), heads(data=Q), 8, 0), F.RopeTensor(heads(data=Q), heads(data=R), 8, 0)]),
+    dict(tensors=[F.RopeTensor(heads(), heads(data=Q), 8, 0), F.RopeTensor(heads(data=R), heads(), 8, 0)])])
 def test_rope_rejects_bad_arguments(kw):
     _expect(F.NVFP4_EINVAL, F.nvfp4_rope, *rope_args(**kw))
 
@@ -97,7 +107,7 @@ def test_rope_helper(calls):
 
 
 def attention_args(**kw):
-    a = dict(q=heads(), k=heads(), v=heads(), out=heads(), batch=2, q_tokens=64, kv_tokens=64, q_heads=8, kv_heads=8,
+    a = dict(q=heads(), k=heads(), v=heads(), out=heads(data=Q), batch=2, q_tokens=64, kv_tokens=64, q_heads=8, kv_heads=8,
              head_dim=64, dtype=0, kv_lens=0, scale=0.125, stream=0)
     a.update(kw)
     return list(a.values())
@@ -108,8 +118,9 @@ def attention_args(**kw):
     dict(head_dim=68), dict(head_dim=136), dict(q_heads=8, kv_heads=3), dict(q_heads=258, kv_heads=2, batch=1),
     dict(dtype=2), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
     dict(scale=3e38), dict(batch=1 << 29, kv_heads=8), dict(q=heads(data=0)), dict(out=heads(data=0)), dict(k=heads(token=4)),
-    dict(v=heads(head=-64)), dict(k=heads(token=0)), dict(q=heads(head=0)), dict(out=heads(batch=0)),
-    dict(out=heads(head=56)), dict(k=heads(batch=1 << 40))])
+    dict(v=heads(head=-64)), dict(k=heads(token=0)), dict(q=heads(head=0)), dict(out=heads(batch=0, data=Q)),
+    dict(out=heads(head=56, data=Q)), dict(k=heads(batch=1 << 40)), dict(out=heads()), dict(q=heads(data=Q)),
+    dict(v=heads(data=Q)), dict(out=heads(token=64, data=Q)), dict(out=heads(batch=63 * 512, data=Q))])
 def test_attention_rejects_bad_arguments(kw):
     _expect(F.NVFP4_EINVAL, F.nvfp4_attention, *attention_args(**kw))
 
@@ -144,3 +155,17 @@ def test_attention_helper(calls):
         with pytest.raises((TypeError, ValueError)):
             bad()
     assert len(calls) == 2
+
+
+@pytest.mark.parametrize("out", [heads(data=Q), heads(token=64, head=64 * 64, data=Q),  # [batch, heads, tokens, width]
+                                 heads(batch=512, token=2 * 512, data=Q),                # [tokens, batch, heads, width]
+                                 heads(batch=64 * 1536, token=1536, data=Q)])            # columns of a wider buffer
+def test_outputs_of_any_order_pass_the_checks(out):
+    if torch.cuda.is_available():
+        pytest.skip("needs a machine without a GPU: the pointers are not real")
+    for call in (lambda: F.nvfp4_attention(*attention_args(out=out)),
+                 lambda: F.nvfp4_rope(*rope_args(tensors=[F.RopeTensor(heads(), out, 8, 0)])),
+                 lambda: F.nvfp4_rope(*rope_args(tensors=[F.RopeTensor(out, out, 8, 0)]))):
+        with pytest.raises(F.NVFP4Error) as e:  # (no device to run on: that, not the arguments, ends the call)
+            call()
+        assert e.value.status in (F.NVFP4_ECUDA, F.NVFP4_EARCH)

@@ -622,7 +622,8 @@ nvfp4_status nvfp4_attention(const nvfp4_heads* q, const nvfp4_heads* k, const n
   p.kv_heads = static_cast<int32_t>(kv_heads);
   p.D = static_cast<int32_t>(head_dim);
   p.group = static_cast<int32_t>(q_heads / kv_heads);
-  p.tile_tokens = 128 / p.group;
+  // (queries that fit 32 rows of a tile take a tile of that many: the kernel may keep four copies)
+  p.tile_tokens = (q_tokens * p.group <= 32 ? 32 : 128) / p.group;
   p.tile_rows = p.tile_tokens * p.group;
   p.q_tiles = (p.q_tokens + p.tile_tokens - 1) / p.tile_tokens;
   p.pairs = (p.q_tiles + 1) / 2;

@@ -49,7 +49,7 @@
 // of 128: 200 us back to back = 1.31 PFLOP/s (0.79 of the measured bf16 burst;
 // under the power cap 236); heads of 64: 180 us (113 are the exponentials' floor);
 // 4096 queries over 512 and 382 states, 24 heads of 128: 59.5 us, a quarter of it
-// between items; one query over 16384 states, 32 heads on 8, batch 4: 54 us.
+// between items.
 // Measured and not kept: a share of the exponentials as a cubic on the FMA pipes
 // (no gain at any share), two threads a row (a vote a tile: the same speed), an
 // output warpgroup of its own (206 us), P handed over in halves.
@@ -59,6 +59,19 @@
 // in turn: each part keeps its own m, sum and O, and they are joined through
 // distributed shared memory in a fixed order (no workspace, no atomics, and the
 // same result every time).
+//
+// Where, besides, those queries are at most 32 rows (kFew: one token, or a few),
+// most of a tile would be rows of nothing, their exponentials the longest part
+// of a step, and all the real ones on one warp of each slot.  Then the Q tile
+// holds the rows four times, once per 32 lanes, and each warp of a slot takes
+// the scores of 32 of the tile's 128 keys for its copy: P of the other keys
+// stays zero, and every copy is a part of its own, with its own m, sum and O,
+// joined within the CTA before the ranks join.  A tile then costs its two
+// products, 0.57 us, instead of 1.05, and the ring has six stages for four.  One
+// query over 16384, 14334, 12284 and 10239 states, 32 heads on 8 of 128: 46.2 us
+// against 53.4 (218 MB: 4.7 TB/s; what is left is the entries' lengths, 41.4 us
+// when they are equal, and 9 us of start, join and end).  33 to 64 rows
+// could have two copies; they have none.
 #include "internal.h"
 
 namespace nvfp4 {
@@ -71,15 +84,18 @@ constexpr int kAttThreads = 384;  // three warpgroups: softmax of each slot, pro
 constexpr uint32_t kPanelBytes = 128 * 128;  // 128 rows of 64 elements, 128-byte swizzle
 
 // kDP: head width rounded up to 64 or 128 (the tensor maps zero-fill the rest).
-template <int kDP>
+// kFew: all queries of a K/V head are at most 32 rows (see the top).
+template <int kDP, bool kFew>
 struct ACfg {
   static constexpr int kPanels = kDP / 64;
   static constexpr uint32_t kTileBytes = kPanels * kPanelBytes;
-  static constexpr int kStages = kDP == 128 ? 4 : 8;
+  // (one Q tile and no panel of O on its way out leave the ring 64 KB more)
+  static constexpr int kQTiles = kFew ? 1 : 2;
+  static constexpr int kStages = kDP == 128 ? (kFew ? 6 : 4) : (kFew ? 11 : 8);
   static constexpr uint32_t kOffQ = 0;
-  static constexpr uint32_t kOffKv = 2 * kTileBytes;
+  static constexpr uint32_t kOffKv = kQTiles * kTileBytes;
   static constexpr uint32_t kOffOut = kOffKv + kStages * kTileBytes;  // a panel of O on its way out, per slot
-  static constexpr uint32_t kOffBar = kOffOut + 2 * kPanelBytes;
+  static constexpr uint32_t kOffBar = kOffOut + (kFew ? 0 : 2 * kPanelBytes);
   // kv_full, kv_empty per stage; q_full, q_empty, s_full, p_ready, pv_done, o_free,
   // o_written, drain per slot; s_free
   static constexpr uint32_t kNumBars = 2 * kStages + 16 + 1;
@@ -90,8 +106,10 @@ struct ACfg {
   static constexpr uint32_t kPartStride = (kDP + 4) * 4;
   static constexpr uint32_t kPartSlot = 128 * kPartStride;
   static constexpr uint32_t kPartMl = 2 * kPartSlot;  // float2 (m, l) [2][128]
-  static_assert(kOffKv + kPartMl + 2 * 128 * 8 <= kOffBar, "the partial results fit");
+  static constexpr uint32_t kPartMlCta = kPartMl + 2 * 128 * 8;  // kFew: the CTA's (m, l) of a row [32]
+  static_assert(kOffKv + kPartMlCta + 32 * 8 <= kOffBar, "the partial results fit");
   static_assert(kSmemBytes <= 232448, "shared memory budget");
+  static_assert(kSmemBytes > 233472 / 2, "one CTA per SM (all 512 TMEM columns are its own)");
 };
 
 // TMEM columns: one S for both slots, P and O of each.
@@ -241,12 +259,12 @@ __device__ __forceinline__ AttItem att_item(const AttentionParams& p, int item, 
   return w;
 }
 
-template <int kDP, bool kFp16>
+template <int kDP, bool kFp16, bool kFew>
 __global__ void __launch_bounds__(kAttThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_o,
                      const __grid_constant__ AttentionParams p) {
-  using C = ACfg<kDP>;
+  using C = ACfg<kDP, kFew>;
   constexpr float kMostSum = 0x1p15f;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -289,10 +307,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  // rows of the Q tiles that no query fills (a group that does not divide 128)
-  for (int t = threadIdx.x; t < 2 * C::kPanels * (128 - p.tile_rows) * 8; t += kAttThreads) {
-    const int chunks = (128 - p.tile_rows) * 8, panel = t / chunks, at = t - panel * chunks;
-    *reinterpret_cast<uint4*>(smem + C::kOffQ + panel * kPanelBytes + p.tile_rows * 128 + at * 16) = make_uint4(0u, 0u, 0u, 0u);
+  // rows of the Q tiles that no query fills (a group that does not divide 128;
+  // kFew: of each of the tile's four copies of up to 32 rows)
+  constexpr int kCopyRows = kFew ? 32 : 128;
+  const int spare = (kCopyRows - p.tile_rows) * 8;  // 16-byte chunks of a copy's panel
+  for (int t = threadIdx.x; t < C::kQTiles * C::kPanels * (128 / kCopyRows) * spare; t += kAttThreads) {
+    const int copy = t / spare, at = t - copy * spare;
+    *reinterpret_cast<uint4*>(smem + C::kOffQ + copy * (kCopyRows * 128) + p.tile_rows * 128 + at * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
   }
   fence_async_smem();
   if (warp == 9 && lane == 0) {
@@ -325,16 +347,17 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   if (warp == 9) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      const uint32_t q_bytes = C::kPanels * static_cast<uint32_t>(p.tile_rows) * 128u;
+      constexpr int kCopies = 128 / kCopyRows;
+      const uint32_t q_bytes = C::kPanels * kCopies * static_cast<uint32_t>(p.tile_rows) * 128u;
       int64_t e = 0;             // ring entries issued
       uint32_t q_phase[2] = {0u, 0u};  // items whose tile went into the slot, mod 2
       bool q_used[2] = {false, false};
       auto load_q = [&](const AttItem& w, int i) {
         if (!mbar_wait(&q_empty[i], q_phase[i] ^ 1u, abort_flag)) return false;
         mbar_arrive_expect_tx(&q_full[i], q_bytes);
-        for (int c = 0; c < C::kPanels; ++c)
-          tma_load_4d(smem + C::kOffQ + i * C::kTileBytes + c * kPanelBytes, &tmap_q, &q_full[i], c * 64,
-                      w.hk * p.group, (w.tile0 + i) * p.tile_tokens, w.b * p.q_bmul);
+        for (int c = 0; c < C::kPanels * kCopies; ++c)
+          tma_load_4d(smem + C::kOffQ + i * C::kTileBytes + c * (kCopyRows * 128), &tmap_q, &q_full[i],
+                      (c / kCopies) * 64, w.hk * p.group, (w.tile0 + i) * p.tile_tokens, w.b * p.q_bmul);
         q_phase[i] ^= 1u;
         q_used[i] = true;
         return true;
@@ -466,6 +489,16 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     const uint32_t t_s = tmem + kColS + t_lane, t_p = tmem + kColP + i * kSlotP + t_lane;
     const uint32_t t_o = tmem + kColO + i * kSlotO + t_lane;
     const float c = p.scale_log2;
+    // this warp's keys of a tile (kFew: its copy of the rows takes a quarter)
+    constexpr int kKeys = kFew ? 32 : 128;
+    constexpr int kHalf = kFew ? 32 : 64;  // keys whose P is made at a time
+    const int key0 = kFew ? (warp & 3) * 32 : 0;
+    if constexpr (kFew) {  // P of the others' keys stays zero
+      const uint32_t zero[16] = {};
+#pragma unroll
+      for (int k = 0; k < 64; k += 16) tmem_st_32x32b_x16(t_p + k, zero);
+      tmem_st_wait();
+    }
     uint32_t s_phase = 0u, pv_phase = 0u, o_phase = 0u;
     RingPos<S> ring;  // of this step's K
     auto all_lanes = [&](bool ok) {
@@ -496,18 +529,23 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         }
         s_phase ^= 1u;
         tc_fence_after();
-        uint32_t r[128];
-        tmem_ld_32x32b_x64(t_s, r);
-        tmem_ld_32x32b_x64(t_s + 64, r + 64);
-        tmem_ld_wait_n<128>(r);
+        uint32_t r[kKeys];
+        if constexpr (kFew) {
+          tmem_ld_32x32b_x32(t_s + key0, r);
+          tmem_ld_wait(r);
+        } else {
+          tmem_ld_32x32b_x64(t_s, r);
+          tmem_ld_32x32b_x64(t_s + 64, r + 64);
+          tmem_ld_wait_n<128>(r);
+        }
         // S is in registers: the next scores, the other slot's, may come
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_free);
         if (valid < kAttTile) {
 #pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (k >= valid) r[k] = 0xFF800000u;  // -inf
+          for (int k = 0; k < kKeys; ++k)
+            if (key0 + k >= valid) r[k] = 0xFF800000u;  // -inf
           if ((i == 0 || w.shared) && (valid & 15) != 0) {
             // the V rows from the last valid state to the next multiple of 16
             // keys: zero, whatever they hold (0 * NaN would not be)
@@ -527,18 +565,18 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         auto row_max = [&]() {
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(r[k]));
+          for (int k = 0; k < kKeys; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(r[k]));
           return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         };
-        // P of the keys from 64 h on with the present reference, two to a word
-        uint32_t pk[32];
+        // P of the keys from kHalf h on with the present reference, two to a word
+        uint32_t pk[kHalf / 2];
         auto make_p = [&](int h, float m) {
           const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-m * c, -m * c);
           uint64_t sum[2] = {0u, 0u};
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
+          for (int k = 0; k < kHalf / 2; ++k) {
             const uint64_t x =
-                f2_fma(f2_pack(__uint_as_float(r[64 * h + 2 * k]), __uint_as_float(r[64 * h + 2 * k + 1])), c2, mc2);
+                f2_fma(f2_pack(__uint_as_float(r[kHalf * h + 2 * k]), __uint_as_float(r[kHalf * h + 2 * k + 1])), c2, mc2);
             float a, b;
             f2_unpack(x, a, b);
             a = exp2_approx(a);
@@ -551,8 +589,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           return a + b;
         };
         auto store_p = [&](int h) {
-          tmem_st_32x32b_x16(t_p + 32 * h, *reinterpret_cast<const uint32_t(*)[16]>(pk));
-          tmem_st_32x32b_x16(t_p + 32 * h + 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16));
+#pragma unroll
+          for (int k = 0; k < kHalf / 2; k += 16)
+            tmem_st_32x32b_x16(t_p + key0 / 2 + (kHalf / 2) * h + k, *reinterpret_cast<const uint32_t(*)[16]>(pk + k));
         };
         // (a row without a finite score so far takes its next tile's maximum)
         if (j == j0 || m_ref == -INFINITY) m_ref = row_max();
@@ -568,7 +607,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           tc_fence_after();
         }
         store_p(0);
-        tile_sum += make_p(1, m_use);
+        if constexpr (!kFew) tile_sum += make_p(1, m_use);
         if (j > j0) {
           const bool moves = tile_sum > kMostSum;
           if (__any_sync(0xffffffffu, moves)) {
@@ -590,10 +629,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             tmem_st_wait();
             tile_sum = make_p(0, m_new);
             store_p(0);
-            tile_sum += make_p(1, m_new);
+            if constexpr (!kFew) tile_sum += make_p(1, m_new);
           }
         }
-        store_p(1);
+        if constexpr (!kFew) store_p(1);
         l_sum += tile_sum;
         tmem_st_wait();
         tc_fence_before();
@@ -609,7 +648,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         pv_phase ^= 1u;
         tc_fence_after();
       }
-      if (p.join) break;  // one item; joined below
+      if (kFew || p.join) break;  // one item; joined below
       // ---- O / sum through shared memory, 64 columns at a time, to the output
       // (zeros where there are no states).  One row a thread straight to global
       // memory took 4200 clocks a tile: every store touched 32 lines.
@@ -694,6 +733,34 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             *reinterpret_cast<uint4*>(dst + d * 4 + k * 16) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
       }
+      if constexpr (kFew) {
+        // the CTA's eight parts of a row (two slots, four copies) become one first
+        named_barrier_sync(2, 256);
+        float2* ml = reinterpret_cast<float2*>(part + C::kPartMl);
+        for (int u = threadIdx.x; u < p.tile_rows * (kDP / 4); u += 256) {
+          const int rr = u / (kDP / 4), g = u - rr * (kDP / 4);
+          float m = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < 8; ++t) m = fmaxf(m, ml[t * 32 + rr].x);
+          float l = 0.0f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const float2 x = ml[t * 32 + rr];
+            if (x.y == 0.0f) continue;  // no keys of its own
+            const float f = exp2_approx((x.x - m) * c);
+            const float4 a = *reinterpret_cast<const float4*>(part + (t * 32 + rr) * C::kPartStride + g * 16);
+            l = fmaf(x.y, f, l);
+            v.x = fmaf(a.x, f, v.x);
+            v.y = fmaf(a.y, f, v.y);
+            v.z = fmaf(a.z, f, v.z);
+            v.w = fmaf(a.w, f, v.w);
+          }
+          // (in the place of the first part: only this thread reads these columns)
+          *reinterpret_cast<float4*>(part + rr * C::kPartStride + g * 16) = v;
+          if (g == 0) reinterpret_cast<float2*>(part + C::kPartMlCta)[rr] = make_float2(m, l);
+        }
+      }
       sync_cluster();
       if (*abort_flag == 0) {
         const int groups = p.D / 8;
@@ -704,12 +771,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           const int i = rr >= rows0 ? 1 : 0;
           const int row = rr - (i ? rows0 : 0);
           // the row's parts: one per rank, or two where the slots shared the tile
-          const int per_rank = w.shared ? 2 : 1;
+          const int per_rank = w.shared && !kFew ? 2 : 1;
           auto part_at = [&](uint32_t base, uint32_t slot_bytes, int t) {
-            const uint32_t a = base + (w.shared ? static_cast<uint32_t>(t & 1) * slot_bytes : 0u);
+            const uint32_t a = base + (per_rank == 2 ? static_cast<uint32_t>(t & 1) * slot_bytes : 0u);
             return peer_smem(a, static_cast<uint32_t>(t / per_rank));
           };
-          const uint32_t ml = smem_u32(part + C::kPartMl + (i * 128 + row) * 8);
+          const uint32_t ml = smem_u32(part + (kFew ? C::kPartMlCta : C::kPartMl) + (i * 128 + row) * 8);
           const uint32_t src = smem_u32(part + i * C::kPartSlot + row * C::kPartStride + g * 32);
           float m = -INFINITY;
           for (int t = 0; t < p.split * per_rank; ++t) m = fmaxf(m, ld_shared_cluster_f2(part_at(ml, 128 * 8, t)).x);
@@ -767,7 +834,7 @@ int resident_clusters(int split, const DeviceInfo& dev) {
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kAttThreads, 1, 1);
     cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms / split * split), 1, 1);
-    cfg.dynamicSmemBytes = ACfg<kDP>::kSmemBytes;
+    cfg.dynamicSmemBytes = ACfg<kDP, false>::kSmemBytes;  // (kFew's too fills an SM)
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(split);
@@ -776,7 +843,7 @@ int resident_clusters(int split, const DeviceInfo& dev) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, attention_kernel<kDP, kFp16>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, attention_kernel<kDP, kFp16, false>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
@@ -785,12 +852,37 @@ int resident_clusters(int split, const DeviceInfo& dev) {
   return n;
 }
 
-template <int kDP, bool kFp16>
-cudaError_t launch(const AttentionMaps& m, AttentionParams p, cudaStream_t stream, const DeviceInfo& dev) {
-  using C = ACfg<kDP>;
-  auto kernel = attention_kernel<kDP, kFp16>;
+template <int kDP, bool kFp16, bool kFew>
+cudaError_t launch_kernel(const AttentionMaps& m, const AttentionParams& p, cudaStream_t stream, const DeviceInfo& dev) {
+  using C = ACfg<kDP, kFew>;
+  auto kernel = attention_kernel<kDP, kFp16, kFew>;
   static SmemLimit limit;
   cudaError_t err = limit.raise(kernel, C::kSmemBytes, dev.device);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kAttThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.split > 1 ? 1 : 0;
+  if (p.items > INT32_MAX / p.split) return cudaErrorInvalidConfiguration;
+  const int ctas = p.join ? p.items * p.split : (p.items < dev.num_sms ? p.items : dev.num_sms);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  err = cudaLaunchKernelEx(&cfg, kernel, m.q, m.k, m.v, m.o, p);
+  if (err != cudaSuccess) return err;
+  return cudaGetLastError();
+}
+
+template <int kDP, bool kFp16>
+cudaError_t launch(const AttentionMaps& m, AttentionParams p, cudaStream_t stream, const DeviceInfo& dev) {
+  // (the occupancy query below needs the limit too)
+  static SmemLimit limit;
+  cudaError_t err = limit.raise(attention_kernel<kDP, kFp16, false>, ACfg<kDP, false>::kSmemBytes, dev.device);
   if (err != cudaSuccess) return err;
   // How an item is shared out, by its cost in key tiles of one slot: whole
   // items in turn, one CTA per SM (kTurnCost for an item's ends), or items with
@@ -815,23 +907,9 @@ cudaError_t launch(const AttentionMaps& m, AttentionParams p, cudaStream_t strea
       p.join = 1;
     }
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kAttThreads, 1, 1);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.split > 1 ? 1 : 0;
-  if (p.items > INT32_MAX / p.split) return cudaErrorInvalidConfiguration;
-  const int ctas = p.join ? p.items * p.split : (p.items < dev.num_sms ? p.items : dev.num_sms);
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
-  err = cudaLaunchKernelEx(&cfg, kernel, m.q, m.k, m.v, m.o, p);
-  if (err != cudaSuccess) return err;
-  return cudaGetLastError();
+  if (p.join != 0 && p.q_tiles == 1 && p.tile_rows <= 32)
+    return launch_kernel<kDP, kFp16, true>(m, p, stream, dev);
+  return launch_kernel<kDP, kFp16, false>(m, p, stream, dev);
 }
 
 }  // namespace

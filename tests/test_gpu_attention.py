@@ -82,6 +82,29 @@ def test_shapes(F, B, Lq, Lk, Hq, Hk, D, dtype):
     assert torch.equal(o, F.cross_attention(q, k, v))  # the same bits again
 
 
+# queries of up to 32 rows a K/V head (tokens x heads) over keys that are shared out, and the first shapes past that
+@pytest.mark.parametrize("B,Lq,Lk,Hq,Hk,D,dtype", [
+    (1, 1, 1025, 1, 1, 128, BF), (2, 32, 1500, 2, 2, 64, HF), (2, 33, 1500, 2, 2, 64, HF), (3, 4, 1700, 40, 5, 128, BF),
+    (1, 10, 3000, 3, 1, 72, BF), (2, 6, 5130, 5, 1, 8, HF), (1, 1, 2049, 32, 1, 128, HF), (1, 1, 2049, 33, 1, 128, HF),
+    (1, 2, 40000, 16, 1, 128, BF), (40, 1, 1900, 8, 8, 64, BF), (25, 3, 1300, 28, 7, 112, HF), (1, 31, 1111, 1, 1, 24, BF)])
+def test_few_queries(F, B, Lq, Lk, Hq, Hk, D, dtype):
+    test_shapes(F, B, Lq, Lk, Hq, Hk, D, dtype)
+
+
+@pytest.mark.parametrize("Lq,Hq,Hk,D,dtype", [(1, 8, 2, 128, BF), (5, 6, 1, 64, HF)])
+@pytest.mark.parametrize("rubbish", [float("nan"), float("-inf")])
+def test_few_queries_over_states_of_many_lengths(F, Lq, Hq, Hk, D, dtype, rubbish):
+    lens = [0, 1, 31, 32, 33, 64, 95, 97, 127, 128, 129, 160, 1000, 1030, 1499, 1500]
+    q, k, v = _rand((16, Lq, Hq, D), dtype, 21), _rand((16, 1500, Hk, D), dtype, 22), _rand((16, 1500, Hk, D), dtype, 23)
+    for b, n in enumerate(lens):
+        k[b, n:] = rubbish
+        v[b, n:] = rubbish
+    lens = torch.tensor(lens, dtype=torch.int32).cuda()
+    o = F.cross_attention(q, k, v, kv_lens=lens)
+    _check(o, q, k, v, lens)
+    assert bool((o[0] == 0).all())
+
+
 LENS = [0, 1, 15, 16, 17, 127, 128, 129, 143, 144, 255, 256, 300, 301, 2 ** 31 - 1, -5]
 
 

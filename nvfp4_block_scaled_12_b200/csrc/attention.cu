@@ -332,6 +332,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   unsigned fault = 0u;
+  // The kernel is launched before the one in front of it has ended, and lets the
+  // next one be: nothing up to here touched global memory.
+  launch_dependents();
+  wait_for_previous_kernel();
 
   // every thread of the item's CTAs
   auto sync_cluster = [&]() {
@@ -863,13 +867,15 @@ cudaError_t launch_kernel(const AttentionMaps& m, const AttentionParams& p, cuda
   cfg.blockDim = dim3(kAttThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.split > 1 ? 1 : 0;
+  cfg.numAttrs = p.split > 1 ? 2 : 1;
   if (p.items > INT32_MAX / p.split) return cudaErrorInvalidConfiguration;
   const int ctas = p.join ? p.items * p.split : (p.items < dev.num_sms ? p.items : dev.num_sms);
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);

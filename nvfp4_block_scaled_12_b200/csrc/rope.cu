@@ -67,6 +67,10 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
   __shared__ double turns[kRopeMaxPairs];  // f_i / 2 pi
   for (int i = threadIdx.x; i < p.R / 2; i += kRopeThreads) turns[i] = p.turns[i];
   __syncthreads();
+  // The kernel is launched before the one in front of it has ended, and lets the
+  // next one be: nothing up to here touched global memory.
+  launch_dependents();
+  wait_for_previous_kernel();
   const int lane = threadIdx.x & (p.group - 1);
   const int64_t u64 = (static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x) / p.group;
   const bool live = u64 < p.units && lane * 8 < p.D;
@@ -178,20 +182,25 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
   }
 }
 
+template <bool kFp16, bool kInterleaved, bool kNorm>
+cudaError_t launch(const RopeParams& p, unsigned blocks, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(kRopeThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, rope_kernel<kFp16, kInterleaved, kNorm>, p);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
 template <bool kFp16>
 cudaError_t launch(const RopeParams& p, unsigned blocks, bool interleaved, bool norm, cudaStream_t stream) {
-  if (interleaved) {
-    if (norm)
-      rope_kernel<kFp16, true, true><<<blocks, kRopeThreads, 0, stream>>>(p);
-    else
-      rope_kernel<kFp16, true, false><<<blocks, kRopeThreads, 0, stream>>>(p);
-  } else {
-    if (norm)
-      rope_kernel<kFp16, false, true><<<blocks, kRopeThreads, 0, stream>>>(p);
-    else
-      rope_kernel<kFp16, false, false><<<blocks, kRopeThreads, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  if (interleaved) return norm ? launch<kFp16, true, true>(p, blocks, stream) : launch<kFp16, true, false>(p, blocks, stream);
+  return norm ? launch<kFp16, false, true>(p, blocks, stream) : launch<kFp16, false, false>(p, blocks, stream);
 }
 
 }  // namespace

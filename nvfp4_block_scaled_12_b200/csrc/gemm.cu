@@ -266,7 +266,10 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16, kMx4>::kT
   tc_fence_after();
   // MXFP4 is launched before the kernel in front of it, its quantizer as a
   // rule, has ended: everything up to here touched no global memory
-  if constexpr (kMx4) wait_for_previous_kernel();
+  if constexpr (kMx4) {
+    launch_dependents();
+    wait_for_previous_kernel();
+  }
   const uint32_t tmem_base = *tmem_slot;
   unsigned fault = 0u;
 

@@ -87,7 +87,11 @@ __global__ void __launch_bounds__(QCfg<kRows>::kThreads, 1)
     fence_mbar_init();
   }
   __syncthreads();
-  if constexpr (kFormat == QFormat::kMxfp4) launch_dependents();  // the GEMM that follows may set itself up
+  if constexpr (kFormat == QFormat::kMxfp4) {
+    // the GEMM that follows may set itself up, as this kernel did beside the one in front of it
+    launch_dependents();
+    wait_for_previous_kernel();
+  }
   unsigned fault = 0u;
   // This CTA's tiles are blockIdx.x + j * gridDim.x, j = 0 .. my_tiles-1.
   // The ring carries a sequence of n_seq loads, entry jj = 4i + g going to
@@ -395,24 +399,26 @@ cudaError_t launch_q(const CUtensorMap& tmap_x, const void* x, int64_t M, int64_
   static SmemLimit limit;
   cudaError_t err = limit.raise(kernel, Q::kSmemBytes, dev.device);
   if (err != cudaSuccess) return err;
-  if (!kDynamic) {
-    kernel<<<grid, Q::kThreads, Q::kSmemBytes, stream>>>(tmap_x, M, K, g, codes, sf, tiles_k, n_tiles, dev.fault,
-                                                         DynamicScaleArgs{});
-    return cudaGetLastError();
-  }
-  // the grid-wide maximum and the arrival counter start at zero
-  err = cudaMemsetAsync(scratch, 0, kDynamicScratchBytes, stream);
-  if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(Q::kThreads, 1, 1);
   cfg.dynamicSmemBytes = Q::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;  // every CTA resident: the grid-wide wait can complete
-  attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (!kDynamic) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (MXFP4 waits for the kernel in front of it)
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = kFormat == QFormat::kMxfp4 ? 1 : 0;
+    err = cudaLaunchKernelEx(&cfg, kernel, tmap_x, M, K, g, codes, sf, tiles_k, n_tiles, dev.fault, DynamicScaleArgs{});
+    return err != cudaSuccess ? err : cudaGetLastError();
+  }
+  // the grid-wide maximum and the arrival counter start at zero
+  err = cudaMemsetAsync(scratch, 0, kDynamicScratchBytes, stream);
+  if (err != cudaSuccess) return err;
+  attr[0].id = cudaLaunchAttributeCooperative;  // every CTA resident: the grid-wide wait can complete
+  attr[0].val.cooperative = 1;
   const DynamicScaleArgs dyn{static_cast<const uint8_t*>(x), scratch, scale_out, wait.limit_ns,
                              static_cast<uint32_t>(grid) + wait.extra_arrivals};
   err = cudaLaunchKernelEx(&cfg, kernel, tmap_x, M, K, 0.0f, codes, sf, tiles_k, n_tiles, dev.fault, dyn);

@@ -312,12 +312,18 @@ def nvfp4_last_error() -> str:
 # --------------------------------------------------------------------------
 
 _torch_module = None
+_empty_strided_cuda = None  # torch's allocation on the current device without the argument parsing (0.8 us, not 2)
 
 
 def _torch():
-    global _torch_module  # (an import statement on every call costs more than the lookup)
+    global _torch_module, _empty_strided_cuda  # (an import statement on every call costs more than the lookup)
     if _torch_module is None:
         import torch
+        if torch.cuda.is_available():
+            try:
+                from torch._C._dynamo.guards import _empty_strided_cuda
+            except ImportError:  # (not in every torch: Tensor.new_empty instead)
+                pass
         _torch_module = torch
     return _torch_module
 
@@ -326,8 +332,8 @@ def _stream(stream) -> int:
     if stream is not None:
         return int(stream.cuda_stream)
     # the current stream's handle without a Stream object around it (7 us of a 22 us call)
-    torch = _torch()
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    C = _torch()._C
+    return C._cuda_getCurrentRawStream(C._cuda_getDevice())
 
 
 def _ptr(t) -> int:
@@ -701,17 +707,22 @@ def _heads(t) -> bytes:
 
 
 def _like(stream, t):
-    """A contiguous new tensor of ``t``'s shape and type, owned by the stream that writes it."""
+    """A contiguous new tensor of the heads tensor ``t``'s shape and type, owned by the stream that writes it."""
     torch = _torch_module or _torch()
     if stream is None:
+        if _empty_strided_cuda is not None:
+            b, l, h, d = t.shape
+            return _empty_strided_cuda((b, l, h, d), (l * h * d, h * d, d, 1), t.dtype)
         return torch.empty_like(t, memory_format=torch.contiguous_format)
     with torch.cuda.stream(stream):
         return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _empty_on(stream, shape, like, dtype):
-    """A new tensor of ``dtype`` on ``like``'s device, owned by the stream that writes it."""
+    """A new tensor of one or two dimensions on ``like``'s, the current device, owned by the stream that writes it."""
     if stream is None:
+        if _empty_strided_cuda is not None:
+            return _empty_strided_cuda(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
         return like.new_empty(shape, dtype=dtype)
     with _torch().cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)

@@ -153,3 +153,45 @@ def test_outputs_given_nothing_is_allocated(F):
     torch.cuda.synchronize()
     assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
     assert torch.cuda.mem_get_info()[0] == free
+
+
+@pytest.mark.parametrize("L", [1, 700])
+def test_calls_in_a_row_equal_calls_one_by_one(F, L):
+    # each kernel sets itself up while the one in front of it ends; every call reads what the last one wrote, into
+    # buffers that the last but one read
+    heads, D = 8, 64
+    gen = torch.Generator("cuda").manual_seed(3)
+    rand = lambda *shape: torch.randn(*shape, device="cuda", generator=gen).to(torch.bfloat16)  # noqa: E731
+    x0, k, v = rand(L, heads * D), rand(1, 1500, heads, D), rand(1, 1500, heads, D)
+    w = F.quantize_mxfp4(rand(heads * D, heads * D) * 0.1)
+    pos = torch.arange(2 * L, device="cuda", dtype=torch.int32).view(L, 2)
+
+    def run(sync):
+        x, y, xq = x0.clone(), torch.empty_like(x0), None
+        turned, o = (torch.empty(1, L, heads, D, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+        for _ in range(30):
+            xq = F.quantize_mxfp4(x, out=xq)
+            sync()
+            F.gemm_mxfp4(xq, w, y=y)
+            sync()
+            F.rope(y.view(1, L, heads, D), pos, [32, 32], q_out=turned)
+            sync()
+            F.rope(turned, pos, [32, 32], q_out=turned)
+            sync()
+            F.cross_attention(turned, k, v, out=o)
+            sync()
+            F.cross_attention(o, k, v, out=x.view(1, L, heads, D))
+            sync()
+            x.add_(x0)
+            sync()
+        return x
+
+    one_by_one = run(torch.cuda.synchronize)
+    for _ in range(3):
+        assert torch.equal(run(lambda: None), one_by_one)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(lambda: None)
+    graph.replay()
+    assert torch.equal(got, one_by_one)
+    F.nvfp4_check_fault()

@@ -13,8 +13,8 @@
 // and cosines are worked out once for all of them and a row's norm is a shuffle
 // within the group.  Lanes load the next four heads before they use the last
 // four, 16 bytes each (two 8-byte halves in the half layout), and four blocks
-// fit an SM.  4608 tokens x 48 heads x 128 with the norms: 22.3 us back to back
-// (5.1 TB/s); 30940 tokens x 24 heads x 128: 59.9 us (6.3 TB/s, 0.97 of a copy).
+// fit an SM.  4608 tokens x 48 heads x 128 with the norms: 18.6 us back to back
+// (6.1 TB/s, 0.93 of a copy); 30940 tokens x 24 heads x 128: 59.9 us (6.3 TB/s, 0.97).
 //
 // The angle is reduced in 64 bits: t = pos * (f_i / 2 pi) turns, of which only
 // t - rint(t) goes on in 32 bits, so a position of a million costs no accuracy
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
   __syncthreads();
   // The kernel is launched before the one in front of it has ended, and lets the
   // next one be: nothing up to here touched global memory.  (Without it call
-  // after call took 24.6 us for the first of these and 62.7 for the second.)
+  // after call took 2.3 us more for the first of these, 2.9 for the second.)
   launch_dependents();
   wait_for_previous_kernel();
   const int lane = threadIdx.x & (p.group - 1);
@@ -92,10 +92,14 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
   const uint16_t* in = static_cast<const uint16_t*>(t.in) + b * t.in_batch + l * t.in_token + head0 * t.in_head;
   uint16_t* out = static_cast<uint16_t*>(t.out) + b * t.out_batch + l * t.out_token + head0 * t.out_head;
   uint4 next[4];
+  // (the pointers step from head to head with the norm, which is bound by its
+  // instructions; without it, bound by memory, that took 62.9 us for 59.8)
   auto load_from = [&](int h0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (h0 + i < nh) next[i] = load_eight(in + (h0 + i) * t.in_head, lo, hi, split);
+    for (int i = 0; i < 4; ++i) {
+      if (h0 + i < nh) next[i] = load_eight(kNorm ? in : in + (h0 + i) * t.in_head, lo, hi, split);
+      if (kNorm) in += t.in_head;
+    }
   };
   load_from(0);
 
@@ -119,16 +123,36 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
       __sincosf(6.2831853f * static_cast<float>(turn - rint(turn)), &sn[j], &cs[j]);
     }
   }
-  float w[8];
+  // A pair (a, b) turns into (ca a - sb b, sa a + cb b): a norm's weights are part
+  // of these, and its root is left for the head.
   const bool normed = kNorm && t.weight != nullptr;
-  if (normed) {
-    const uint4 x = live ? load_eight(static_cast<const uint16_t*>(t.weight), lo, hi, split) : make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+  float ca[4], sb[4], sa[4], cb[4];
+  if constexpr (kNorm) {
+    float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    if (normed && live) {
+      const uint4 x = load_eight(static_cast<const uint16_t*>(t.weight), lo, hi, split);
+      const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = unpack2<kFp16>(xw[j]);
+        w[2 * j] = v.x;
+        w[2 * j + 1] = v.y;
+      }
+    }
+    const bool apart = !kInterleaved && rotary;  // a pair's elements are four apart, not neighbours
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 v = unpack2<kFp16>(xw[j]);
-      w[2 * j] = v.x;
-      w[2 * j + 1] = v.y;
+      const float wa = apart ? w[j] : w[2 * j], wb = apart ? w[j + 4] : w[2 * j + 1];
+      ca[j] = cs[j] * wa;
+      sb[j] = sn[j] * wb;
+      sa[j] = sn[j] * wa;
+      cb[j] = cs[j] * wb;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      ca[j] = cb[j] = cs[j];
+      sa[j] = sb[j] = sn[j];
     }
   }
 
@@ -154,31 +178,36 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
         ss = use ? ss : 0.0f;  // (lanes past the width take part with nothing)
-        for (int o = p.group >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          if (p.group > o) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         if (normed) {
           const float r = rsqrtf(ss * p.inv_d + p.eps);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] *= r * w[j];
+          for (int j = 0; j < 8; ++j) v[j] *= r;
         }
       }
-      if (!use) continue;
+      if (!kNorm && !use) continue;
       uint32_t y[4];
       if (kInterleaved || !rotary) {
-        // (lanes that pass through have cosines of 1 and sines of 0)
+        // (lanes that pass through have cosines of 1: times the weight, or as they are)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          y[j] = rotary ? pack2<kFp16>(v[2 * j] * cs[j] - v[2 * j + 1] * sn[j], v[2 * j] * sn[j] + v[2 * j + 1] * cs[j])
-                        : pack2<kFp16>(v[2 * j], v[2 * j + 1]);
+          y[j] = rotary  ? pack2<kFp16>(ca[j] * v[2 * j] - sb[j] * v[2 * j + 1], sa[j] * v[2 * j] + cb[j] * v[2 * j + 1])
+                 : kNorm ? pack2<kFp16>(ca[j] * v[2 * j], cb[j] * v[2 * j + 1])
+                         : pack2<kFp16>(v[2 * j], v[2 * j + 1]);
       } else {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          y[j] = pack2<kFp16>(v[2 * j] * cs[2 * j] - v[2 * j + 4] * sn[2 * j],
-                              v[2 * j + 1] * cs[2 * j + 1] - v[2 * j + 5] * sn[2 * j + 1]);
-          y[j + 2] = pack2<kFp16>(v[2 * j] * sn[2 * j] + v[2 * j + 4] * cs[2 * j],
-                                  v[2 * j + 1] * sn[2 * j + 1] + v[2 * j + 5] * cs[2 * j + 1]);
+          y[j] = pack2<kFp16>(ca[2 * j] * v[2 * j] - sb[2 * j] * v[2 * j + 4],
+                              ca[2 * j + 1] * v[2 * j + 1] - sb[2 * j + 1] * v[2 * j + 5]);
+          y[j + 2] = pack2<kFp16>(sa[2 * j] * v[2 * j] + cb[2 * j] * v[2 * j + 4],
+                                  sa[2 * j + 1] * v[2 * j + 1] + cb[2 * j + 1] * v[2 * j + 5]);
         }
       }
-      store_eight(out + (h0 + i) * t.out_head, lo, hi, split, make_uint4(y[0], y[1], y[2], y[3]));
+      if (use)
+        store_eight(kNorm ? out : out + (h0 + i) * t.out_head, lo, hi, split, make_uint4(y[0], y[1], y[2], y[3]));
+      if (kNorm) out += t.out_head;
     }
   }
 }

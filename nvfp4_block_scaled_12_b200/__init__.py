@@ -245,6 +245,7 @@ def nvfp4_fp8row_gemm(a: int, a_scale: int, b: int, b_scale: int, M: int, N: int
 
 _HEADS = struct.Struct("@P3q")          # nvfp4_heads
 _ROPE_TENSOR = struct.Struct("@P3qP3qqP")  # nvfp4_rope_tensor
+_ROPE_TAIL = struct.Struct("@qP")          # what follows its two nvfp4_heads
 
 
 def _address(x):
@@ -548,9 +549,15 @@ def _mxfp4_sf_bytes(rows, k):
 
 
 def _need_mxfp4(t, name, rows, k, dev):
-    torch = _torch()
+    torch = _torch_module or _torch()
     if t.rows != rows or t.k != k:
         raise ValueError(f"{name} is [{t.rows}, {t.k}], [{rows}, {k}] needed")
+    c, s, u8 = t.codes, t.sf, torch.uint8
+    # (all that _need looks at, in one expression: a call of these helpers is a dozen microseconds)
+    if (type(c) is torch.Tensor and type(s) is torch.Tensor and c.dtype is u8 and s.dtype is u8
+            and c.get_device() == dev and s.get_device() == dev and c.is_contiguous() and s.is_contiguous()
+            and c.numel() >= rows * k // 2 and s.numel() >= _mxfp4_sf_bytes(rows, k)):
+        return
     _need(t.codes, torch.uint8, None, f"{name}.codes", rows * k // 2, dev=dev)
     _need(t.sf, torch.uint8, None, f"{name}.sf", _mxfp4_sf_bytes(rows, k), dev=dev)
 
@@ -700,28 +707,35 @@ def _need_heads(t, name, dev, dtype=None, shape=None):
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _heads(t) -> bytes:
-    """``t`` [batch, tokens, heads, head_dim] as the bytes of an nvfp4_heads."""
-    sb, st, sh, _ = t.stride()
-    return _HEADS.pack(t.data_ptr(), sb, st, sh)
+def _heads(t, name, dev, dtype=None, shape=None) -> bytes:
+    """``t`` [batch, tokens, heads, head_dim], once ``_need_heads`` has nothing
+    against it, as the bytes of an nvfp4_heads."""
+    torch = _torch_module or _torch()
+    stride = t.stride() if type(t) is torch.Tensor else ()
+    # (all that _need_heads looks at, in one expression)
+    if not (len(stride) == 4 and stride[3] == 1 and t.get_device() == dev and t.numel() != 0
+            and (t.dtype is dtype if dtype is not None else t.dtype is torch.bfloat16 or t.dtype is torch.float16)
+            and (shape is None or t.shape == shape)):
+        _need_heads(t, name, dev, dtype, shape)
+        stride = t.stride()
+    return _HEADS.pack(t.data_ptr(), stride[0], stride[1], stride[2])
 
 
 def _like(stream, t):
-    """A contiguous new tensor of the heads tensor ``t``'s shape and type, owned by the stream that writes it."""
-    torch = _torch_module or _torch()
-    if stream is None:
-        if _empty_strided_cuda is not None:
-            b, l, h, d = t.shape
-            return _empty_strided_cuda((b, l, h, d), (l * h * d, h * d, d, 1), t.dtype)
-        return torch.empty_like(t, memory_format=torch.contiguous_format)
-    with torch.cuda.stream(stream):
-        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    """A contiguous new tensor of the heads tensor ``t``'s shape and type, owned
+    by the stream that writes it, and its nvfp4_heads."""
+    b, l, h, d = t.shape
+    if stream is None and _empty_strided_cuda is not None:
+        out = _empty_strided_cuda((b, l, h, d), (l * h * d, h * d, d, 1), t.dtype)
+    else:
+        out = _empty_on(stream, (b, l, h, d), t, t.dtype)
+    return out, _HEADS.pack(out.data_ptr(), l * h * d, h * d, d)
 
 
 def _empty_on(stream, shape, like, dtype):
-    """A new tensor of one or two dimensions on ``like``'s, the current device, owned by the stream that writes it."""
+    """A new tensor on ``like``'s, the current device, owned by the stream that writes it."""
     if stream is None:
-        if _empty_strided_cuda is not None:
+        if _empty_strided_cuda is not None and len(shape) <= 2:
             return _empty_strided_cuda(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
         return like.new_empty(shape, dtype=dtype)
     with _torch().cuda.stream(stream):
@@ -743,7 +757,7 @@ def rope(q, positions, axes: Sequence[int], k=None, theta: float = 10000.0, q_we
     the results (the inputs themselves, to work in place)."""
     torch = _torch()
     dev = torch.cuda.current_device()
-    _need_heads(q, "q", dev)
+    q_heads = _heads(q, "q", dev)
     B, L, _, D = q.shape
     dtype, n = q.dtype, len(axes)
     if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.float32):
@@ -751,26 +765,25 @@ def rope(q, positions, axes: Sequence[int], k=None, theta: float = 10000.0, q_we
     if positions.shape != (L, n) and positions.shape != (B, L, n):
         raise ValueError(f"positions must be [{L}, {n}] or [{B}, {L}, {n}], got {tuple(positions.shape)}")
     _need(positions, positions.dtype, None, "positions", dev=dev)
-
-    def tensor(x, name, weight, out):
-        if weight is not None:
-            _need(weight, dtype, (D,), f"{name}_weight", dev=dev)
-        if out is None:
-            out = _like(stream, x)
-        else:
-            _need_heads(out, f"{name}_out", dev, dtype, x.shape)
-        ib, it, ih, _ = x.stride()
-        ob, ot, oh, _ = out.stride()
-        return out, _ROPE_TENSOR.pack(x.data_ptr(), ib, it, ih, out.data_ptr(), ob, ot, oh, x.shape[2], _ptr(weight))
-
     if k is not None:
-        _need_heads(k, "k", dev, dtype, (B, L, k.shape[2] if k.dim() == 4 else 0, D))
+        k_heads = _heads(k, "k", dev, dtype, (B, L, k.shape[2] if k.dim() == 4 else 0, D))
+        if k_weight is not None:
+            _need(k_weight, dtype, (D,), "k_weight", dev=dev)
     elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight and k_out need k")
-    q_out, tensors = tensor(q, "q", q_weight, q_out)
+    if q_weight is not None:
+        _need(q_weight, dtype, (D,), "q_weight", dev=dev)
+    if q_out is None:
+        q_out, out_heads = _like(stream, q)
+    else:
+        out_heads = _heads(q_out, "q_out", dev, dtype, q.shape)
+    tensors = q_heads + out_heads + _ROPE_TAIL.pack(q.shape[2], _ptr(q_weight))
     if k is not None:
-        k_out, k_tensor = tensor(k, "k", k_weight, k_out)
-        tensors += k_tensor
+        if k_out is None:
+            k_out, out_heads = _like(stream, k)
+        else:
+            out_heads = _heads(k_out, "k_out", dev, dtype, k.shape)
+        tensors += k_heads + out_heads + _ROPE_TAIL.pack(k.shape[2], _ptr(k_weight))
     nvfp4_rope(tensors, B, L, D, DTYPE_FP16 if dtype == torch.float16 else DTYPE_BF16, positions.data_ptr(),
                POS_FLOAT32 if positions.dtype == torch.float32 else POS_INT32, L * n if positions.dim() == 3 else 0,
                axes, float(theta), ROPE_INTERLEAVED * bool(interleaved) + ROPE_SHARED_LADDER * bool(shared),
@@ -789,20 +802,23 @@ def cross_attention(q, k, v, kv_lens=None, scale: Optional[float] = None, out=No
     default.  k and v may be views expanded over the batch."""
     torch = _torch()
     dev = torch.cuda.current_device()
-    _need_heads(q, "q", dev)
+    qh = _heads(q, "q", dev)
+    dtype = q.dtype
+    kh = _heads(k, "k", dev, dtype)
+    kv_shape = k.shape
+    vh = _heads(v, "v", dev, dtype, kv_shape)
     B, Lq, Hq, D = q.shape
-    _need_heads(k, "k", dev, q.dtype)
-    _need_heads(v, "v", dev, q.dtype, k.shape)
-    if k.shape[0] != B or k.shape[3] != D:
-        raise ValueError(f"k must be [{B}, tokens, heads, {D}], got {tuple(k.shape)}")
+    Bk, Lk, Hk, Dk = kv_shape
+    if Bk != B or Dk != D:
+        raise ValueError(f"k must be [{B}, tokens, heads, {D}], got {tuple(kv_shape)}")
     if kv_lens is not None:
         _need(kv_lens, torch.int32, (B,), "kv_lens", dev=dev)
     if out is None:
-        out = _like(stream, q)
+        out, oh = _like(stream, q)
     else:
-        _need_heads(out, "out", dev, q.dtype, q.shape)
-    nvfp4_attention(_heads(q), _heads(k), _heads(v), _heads(out), B, Lq, k.shape[1], Hq, k.shape[2], D,
-                    DTYPE_FP16 if q.dtype == torch.float16 else DTYPE_BF16, _ptr(kv_lens),
+        oh = _heads(out, "out", dev, dtype, q.shape)
+    nvfp4_attention(qh, kh, vh, oh, B, Lq, Lk, Hq, Hk, D,
+                    DTYPE_FP16 if dtype == torch.float16 else DTYPE_BF16, _ptr(kv_lens),
                     D ** -0.5 if scale is None else float(scale), _stream(stream))
     return out
 

@@ -48,7 +48,7 @@
 // with an MMA issuer are the slow ones.  Joint attention of 4608 tokens, 24 heads
 // of 128: 200 us back to back = 1.31 PFLOP/s (0.79 of the measured bf16 burst;
 // under the power cap 236); heads of 64: 180 us (113 are the exponentials' floor);
-// 4096 queries over 512 and 382 states, 24 heads of 128: 59.5 us, a quarter of it
+// 4096 queries over 512 and 382 states, 24 heads of 128: 57 us, a quarter of it
 // between items.
 // Measured and not kept: a share of the exponentials as a cubic on the FMA pipes
 // (no gain at any share), two threads a row (a vote a tile: the same speed), an
@@ -70,7 +70,9 @@
 // products, 0.57 us, instead of 1.05, and the ring has six stages for four.  One
 // query over 16384, 14334, 12284 and 10239 states, 32 heads on 8 of 128: 43.4 us
 // (218 MB: 5.0 TB/s) against 50.5; what is left is that the longest entry's CTAs end
-// last (2 to 3 us) and 9 us of start, join and end.  33 to 64 rows could have two
+// last (2 to 3 us) and 9 us of start, join and end.  32 entries of 4096 states each:
+// 87.5 us = 6.1 TB/s, 0.94 of a copy; short items pay their start and join (64
+// entries of 1024 states, 16 heads of 64: 3.1 TB/s).  33 to 64 rows could have two
 // copies; they have none.
 #include "internal.h"
 

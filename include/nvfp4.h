@@ -660,6 +660,21 @@ nvfp4_status nvfp4_gemm_plan(int64_t M, int64_t N, int64_t K, int32_t num_sms, i
  */
 int32_t nvfp4_quantize_tile_rows(int64_t M, int64_t K, int32_t num_sms);
 
+/*
+ * How nvfp4_rope shares out its work on a device with num_sms SMs, for one
+ * tensor of heads0 heads and, with heads1 > 0, a second one, over `tokens`
+ * tokens (batch * tokens of the call) of heads of head_dim (host only): the
+ * heads of a tensor and token are cut into units, each the work of one group
+ * of lanes, which share their sines and cosines:
+ *   out[0], out[1] = heads of a unit of the first and the second tensor (the
+ *                    last unit of a token may have fewer),
+ *   out[2], out[3] = units of a token in the first and the second tensor
+ * (0 for a second tensor that is not there).  Errors: EINVAL (null out, sizes
+ * out of range).
+ */
+nvfp4_status nvfp4_rope_plan(int64_t heads0, int64_t heads1, int64_t tokens, int64_t head_dim,
+                             int32_t num_sms, int32_t* out);
+
 /* Message describing the last error of the calling thread ("" if none).
  * The pointer stays valid until the thread's next call into the library. */
 const char* nvfp4_last_error(void);

@@ -103,13 +103,14 @@ def _load() -> ctypes.CDLL:
     lib.nvfp4_gemm_plan.argtypes = [i64, i64, i64, i32, i32, ctypes.POINTER(ctypes.c_int32)]
     lib.nvfp4_quantize_tile_rows.argtypes = [i64, i64, i32]
     lib.nvfp4_quantize_tile_rows.restype = ctypes.c_int32
+    lib.nvfp4_rope_plan.argtypes = [i64, i64, i64, i64, i32, ctypes.POINTER(ctypes.c_int32)]
     for name in ("nvfp4_calibrate", "nvfp4_quantize", "nvfp4_swizzle_sf", "nvfp4_gemm", "nvfp4_gemm_quant",
                  "nvfp4_quantize_dynamic", "nvfp4_gemm_dynamic", "nvfp4_quantize_dynamic_noalloc",
                  "nvfp4_mxfp8_quantize", "nvfp4_mxfp8_gemm", "nvfp4_fp8row_quantize", "nvfp4_fp8row_gemm",
                  "nvfp4_dequantize", "nvfp4_check_fault", "nvfp4_gemm_tile_shape", "nvfp4_gemm_scaled",
                  "nvfp4_gemm_quant_scaled", "nvfp4_testing_set_grid_wait", "nvfp4_w4a16_gemm",
                  "nvfp4_gemm_plan", "nvfp4_gemm_amax", "nvfp4_quantize_from_amax", "nvfp4_mxfp4_quantize",
-                 "nvfp4_mxfp4_gemm", "nvfp4_rope", "nvfp4_attention"):
+                 "nvfp4_mxfp4_gemm", "nvfp4_rope", "nvfp4_rope_plan", "nvfp4_attention"):
         getattr(lib, name).restype = ctypes.c_int
     lib.nvfp4_last_error.argtypes = []
     lib.nvfp4_last_error.restype = ctypes.c_char_p
@@ -302,6 +303,14 @@ def nvfp4_gemm_plan(M: int, N: int, K: int, num_sms: int, w4a16: int = 0) -> tup
 
 def nvfp4_quantize_tile_rows(M: int, K: int, num_sms: int) -> int:
     return int(library().nvfp4_quantize_tile_rows(M, K, num_sms))
+
+
+def nvfp4_rope_plan(heads0: int, heads1: int, tokens: int, head_dim: int, num_sms: int) -> tuple:
+    """(heads of a unit of the first and second tensor, units of a token in
+    the first and second) that rope takes; heads1 = 0 for one tensor."""
+    out = (ctypes.c_int32 * 4)()
+    _check(library().nvfp4_rope_plan(heads0, heads1, tokens, head_dim, num_sms, out))
+    return tuple(out)
 
 
 def nvfp4_last_error() -> str:

@@ -1046,6 +1046,26 @@ int32_t nvfp4_quantize_tile_rows(int64_t M, int64_t K, int32_t num_sms) {
   return quantize_tile_rows(M, K, num_sms);
 }
 
+nvfp4_status nvfp4_rope_plan(int64_t heads0, int64_t heads1, int64_t tokens, int64_t head_dim, int32_t num_sms,
+                             int32_t* out) {
+  if (!out) return fail(NVFP4_EINVAL, "null output pointer");
+  if (heads0 < 1 || heads0 > 65535 || heads1 < 0 || heads1 > 65535 || tokens < 1 || tokens > kMaxDim || head_dim < 8 ||
+      head_dim % 8 != 0 || head_dim > 2 * kRopeMaxPairs || num_sms < 1)
+    return fail(NVFP4_EINVAL, "heads0=%lld, heads1=%lld, tokens=%lld, head_dim=%lld, num_sms=%d out of range",
+                (long long)heads0, (long long)heads1, (long long)tokens, (long long)head_dim, num_sms);
+  RopeParams p = {};
+  p.t[0].heads = static_cast<int32_t>(heads0);
+  p.t[1].heads = static_cast<int32_t>(heads1);
+  p.D = static_cast<int32_t>(head_dim);
+  int64_t blocks = 0;
+  if (!rope_plan(&p, tokens, num_sms, &blocks)) return fail(NVFP4_EINVAL, "problem too large");
+  out[0] = p.t[0].heads_per_unit;
+  out[1] = p.t[1].heads_per_unit;
+  out[2] = p.parts0;
+  out[3] = p.units_per_token - p.parts0;
+  return ok();
+}
+
 const char* nvfp4_last_error(void) { return t_last_error.c_str(); }
 
 }  // extern "C"

@@ -616,6 +616,18 @@ nvfp4_status nvfp4_attention(const nvfp4_heads* q, const nvfp4_heads* k, const n
   p.out_batch = batch > 1 ? out->batch_stride : 0;
   p.out_token = q_tokens > 1 ? out->token_stride : 0;
   p.out_head = q_heads > 1 ? out->head_stride : 0;
+  p.q = q->data;
+  p.q_batch = batch > 1 ? q->batch_stride : 0;
+  p.q_token = q_tokens > 1 ? q->token_stride : 0;
+  p.q_head = q_heads > 1 ? q->head_stride : 0;
+  p.k = k->data;
+  p.k_batch = batch > 1 ? k->batch_stride : 0;
+  p.k_token = kv_tokens > 1 ? k->token_stride : 0;
+  p.k_head = kv_heads > 1 ? k->head_stride : 0;
+  p.v = v->data;
+  p.v_batch = batch > 1 ? v->batch_stride : 0;
+  p.v_token = kv_tokens > 1 ? v->token_stride : 0;
+  p.v_head = kv_heads > 1 ? v->head_stride : 0;
   p.kv_lens = kv_lens;
   p.q_tokens = static_cast<int32_t>(q_tokens);
   p.kv_tokens = static_cast<int32_t>(kv_tokens);

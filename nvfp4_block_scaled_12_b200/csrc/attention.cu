@@ -66,7 +66,8 @@
 // holds the rows four times, once per 32 lanes, and each warp of a slot takes
 // the scores of 32 of the tile's 128 keys for its copy: P of the other keys
 // stays zero, and every copy is a part of its own, with its own m, sum and O,
-// joined within the CTA before the ranks join.  A tile then costs its two
+// joined within the CTA before the ranks join (a row that an infinite V turned
+// into NaN that way is made once more, few_rows_again).  A tile then costs its two
 // products, 0.57 us, instead of 1.05, and the ring has six stages for four.  One
 // query over 16384, 14334, 12284 and 10239 states, 32 heads on 8 of 128: 43.4 us
 // (218 MB: 5.0 TB/s) against 50.5; what is left is that the longest entry's CTAs end
@@ -232,6 +233,13 @@ struct RingPos {
   }
 };
 
+// Two 16-bit elements of a word, the low half first.
+template <bool kFp16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (kFp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+
 // One work item as every role sees it.
 struct AttItem {
   int b, hk, tile0;    // batch entry, K/V head, first query tile
@@ -261,6 +269,91 @@ __device__ __forceinline__ AttItem att_item(const AttentionParams& p, int item, 
   return w;
 }
 
+// kFew: rows of the CTA's joined parts (a bit each) once more where they hold NaN
+// though their scores are numbers.  A copy of a row multiplies all keys of a tile,
+// with probabilities of zero for the other copies' keys, and 0 * inf is NaN: for
+// an infinite V that is the form's doing and not the definition's.  So the eight
+// softmax warps take the CTA's keys in turn, each key with its own probability
+// alone, and the columns that were NaN get their sum, in a fixed order: inf, or
+// NaN where the definition has it too.  A way off the tensor cores: one query of
+// 32 heads on 8 over 16384 states, four entries, takes 0.48 ms with an infinity in
+// one state and 0.65 with one in every state, for 0.042.  Rows without an infinite
+// or undefined V never come here; a function of its own, out of the way and with
+// nothing of the kernel's passed in memory, costs them 0.3 us (inlined 0.7, with
+// the item by reference 1.5).
+template <int kDP, bool kFp16, typename C>
+__device__ __noinline__ void few_rows_again(const AttentionParams& p, int item, int rank, unsigned rows, uint8_t* part) {
+  constexpr int kWords = kDP / 64;  // of two elements: a lane's share of a row of V
+  const AttItem w = att_item(p, item, rank);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int col = lane * 2 * kWords;
+  const uint16_t* k = static_cast<const uint16_t*>(p.k) + w.b * p.k_batch + w.hk * p.k_head;
+  const uint16_t* v = static_cast<const uint16_t*>(p.v) + w.b * p.v_batch + w.hk * p.v_head + col;
+  const int end = min(w.len, (w.kt0 + w.n) * kAttTile);
+  for (; rows != 0u; rows &= rows - 1u) {
+    const int row = __ffs(static_cast<int>(rows)) - 1;
+    const float mc = reinterpret_cast<const float2*>(part + C::kPartMlCta)[row].x * p.scale_log2;
+    const uint16_t* q = static_cast<const uint16_t*>(p.q) + w.b * p.q_batch + (row / p.group) * p.q_token +
+                        (w.hk * p.group + row % p.group) * p.q_head;
+    float2 sum[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) sum[i] = make_float2(0.0f, 0.0f);
+    // 32 keys a turn: a lane's own key's score, then the keys' V one after another
+    for (int key0 = w.kt0 * kAttTile + warp * 32; key0 < end; key0 += 8 * 32) {
+      float e = 0.0f;
+      if (key0 + lane < end) {
+        float s = 0.0f;
+#pragma unroll 4
+        for (int d = 0; d < p.D; d += 8) {
+          const uint4 x = *reinterpret_cast<const uint4*>(k + (key0 + lane) * p.k_token + d);
+          const uint4 y = *reinterpret_cast<const uint4*>(q + d);
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 a = unpack2<kFp16>(xw[i]), b = unpack2<kFp16>(yw[i]);
+            s = fmaf(a.x, b.x, fmaf(a.y, b.y, s));
+          }
+        }
+        e = exp2_approx(fmaf(s, p.scale_log2, -mc));
+      }
+      __syncwarp();
+      const int n = min(32, end - key0);
+#pragma unroll 8
+      for (int t = 0; t < n; ++t) {
+        const float et = __shfl_sync(0xffffffffu, e, t);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          float2 x = make_float2(0.0f, 0.0f);
+          if (col < p.D) x = unpack2<kFp16>(reinterpret_cast<const uint32_t*>(v + (key0 + t) * p.v_token)[i]);
+          sum[i].x = fmaf(et, x.x, sum[i].x);
+          sum[i].y = fmaf(et, x.y, sum[i].y);
+        }
+      }
+    }
+    // (the joined row took the first part's place; the seven others of the row are read no more)
+    auto part_of = [&](int t) { return reinterpret_cast<float2*>(part + (t * 32 + row) * C::kPartStride + col * 4); };
+    if (warp > 0) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) part_of(warp)[i] = sum[i];
+    }
+    named_barrier_sync(2, 256);
+    if (warp == 0) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        float2 x = part_of(0)[i];
+        for (int t = 1; t < 8; ++t) {
+          sum[i].x += part_of(t)[i].x;
+          sum[i].y += part_of(t)[i].y;
+        }
+        x.x = isnan(x.x) ? sum[i].x : x.x;
+        x.y = isnan(x.y) ? sum[i].y : x.y;
+        part_of(0)[i] = x;
+      }
+    }
+  }
+}
+
 template <int kDP, bool kFp16, bool kFew>
 __global__ void __launch_bounds__(kAttThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
@@ -284,6 +377,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
   uint64_t* s_free = drain + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  unsigned* again = reinterpret_cast<unsigned*>(smem + C::kOffMisc + 8);  // kFew: rows to make once more, a bit each
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -307,6 +401,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     }
     mbar_init(s_free, 4);  // the four softmax warps that read S
     *abort_flag = 0;
+    *again = 0u;
     fence_mbar_init();
   }
   // rows of the Q tiles that no query fills (a group that does not divide 128;
@@ -744,7 +839,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         // the CTA's eight parts of a row (two slots, four copies) become one first
         named_barrier_sync(2, 256);
         float2* ml = reinterpret_cast<float2*>(part + C::kPartMl);
-        for (int u = threadIdx.x; u < p.tile_rows * (kDP / 4); u += 256) {
+        bool any = false;
+        const int queries = p.q_tokens * p.group;  // (the tile's rows behind them are nobody's)
+        for (int u = threadIdx.x; u < queries * (kDP / 4); u += 256) {
           const int rr = u / (kDP / 4), g = u - rr * (kDP / 4);
           float m = -INFINITY;
 #pragma unroll
@@ -766,7 +863,13 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           // (in the place of the first part: only this thread reads these columns)
           *reinterpret_cast<float4*>(part + rr * C::kPartStride + g * 16) = v;
           if (g == 0) reinterpret_cast<float2*>(part + C::kPartMlCta)[rr] = make_float2(m, l);
+          if (!isnan(l) && (isnan(v.x) || isnan(v.y) || isnan(v.z) || isnan(v.w))) {
+            atomicOr(again, 1u << rr);
+            any = true;
+          }
         }
+        if (__builtin_expect(named_barrier_any(2, 256, any), 0))
+          few_rows_again<kDP, kFp16, C>(p, first, rank, *again, part);
       }
       sync_cluster();
       if (*abort_flag == 0) {

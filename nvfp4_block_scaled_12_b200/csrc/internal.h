@@ -187,6 +187,8 @@ cudaError_t launch_rope(const RopeParams& p, int64_t blocks, bool fp16, bool int
 struct AttentionParams {
   void* out;
   int64_t out_batch, out_token, out_head;
+  const void *q, *k, *v;  // what the tensor maps cover, for plain loads
+  int64_t q_batch, q_token, q_head, k_batch, k_token, k_head, v_batch, v_token, v_head;
   const int32_t* kv_lens;  // nullable: all kv_tokens states are valid
   int32_t q_tokens, kv_tokens, kv_heads, D;
   int32_t group;                    // query heads per K/V head

@@ -511,7 +511,9 @@ nvfp4_status nvfp4_rope(const nvfp4_rope_tensor* tensors, int32_t n_tensors,
  *              Infinities among the valid v give what the sum gives: inf of
  *              their sign, NaN where both signs meet, and NaN too where the
  *              probability rounds to zero (in fp16, below 2^-25 of the largest).
- *   scale      positive and finite (1 / sqrt(head_dim) as a rule)
+ *   scale      positive and finite (1 / sqrt(head_dim) as a rule).  A score
+ *              that it takes out of fp32's range counts as that infinity: -inf
+ *              has a probability of zero, +inf makes its query NaN.
  * Every extent >= 1; head_dim a multiple of 8, at most 128; q_heads a multiple
  * of kv_heads, at most 128 of them to a K/V head; out overlaps no input.  The
  * same inputs give the same bits.  Errors: EINVAL, EALIGN, EARCH, ECUDA; a

@@ -668,7 +668,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int k = 0; k < kKeys; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(r[k]));
-          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // A score that its scale takes out of fp32's range counts as that infinity:
+          // -inf has a probability of zero, +inf makes the row NaN (with -c m infinite
+          // every exponent would be, and P zero or infinite for finite scores)
+          const float x = m * c;
+          return fabsf(x) == INFINITY ? (x < 0.0f ? x : NAN) : m;
         };
         // P of the keys from kHalf h on with the present reference, two to a word
         uint32_t pk[kHalf / 2];

@@ -258,7 +258,7 @@ __device__ __forceinline__ AttItem att_item(const AttentionParams& p, int item, 
   w.tile0 = 2 * pair;
   w.slots = min(2, p.q_tiles - w.tile0);
   w.shared = p.join != 0 && p.q_tiles == 1;
-  w.len = p.kv_lens != nullptr ? min(max(__ldg(p.kv_lens + w.b), 0), p.kv_tokens) : p.kv_tokens;
+  w.len = p.kv_lens != nullptr ? min(max(ld_after_wait(p.kv_lens + w.b), 0), p.kv_tokens) : p.kv_tokens;
   const unsigned tiles = (static_cast<unsigned>(w.len) + kAttTile - 1) / kAttTile;  // (at most 2^23)
   w.kt0 = 0;
   w.n = static_cast<int>(tiles);

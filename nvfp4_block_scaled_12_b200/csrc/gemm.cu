@@ -188,6 +188,13 @@ __device__ __forceinline__ void store_chunk_bf16(const CUtensorMap* tmap, uint8_
   }
 }
 
+// Bias values; kEarly: in a kernel launched before the one in front of it has ended.
+template <bool kEarly, typename V>
+__device__ __forceinline__ V ld_bias(const V* p) {
+  if constexpr (kEarly) return ld_after_wait(p);
+  else return __ldg(p);
+}
+
 template <int kCG, int kBN, int kAcc, bool kFused, bool kMx, bool kRow, bool kW16 = false, bool kMx4 = false>
 __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16, kMx4>::kThreads, 1)
     gemm_nvf4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
@@ -789,7 +796,7 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16, kMx4>::kT
       {
         uint2 bv = make_uint2(0u, 0u);
         const int cb = c0 + lane * 4;
-        if (p.bias != nullptr && cb < p.N) bv = __ldg(reinterpret_cast<const uint2*>(p.bias + cb));
+        if (p.bias != nullptr && cb < p.N) bv = ld_bias<kMx4>(reinterpret_cast<const uint2*>(p.bias + cb));
         *reinterpret_cast<uint2*>(bias_buf + lane * 8) = bv;
       }
       const bool got = mbar_wait(&acc_full[0], acc_phase, abort_flag);
@@ -918,7 +925,7 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16, kMx4>::kT
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           uint4 b = make_uint4(0u, 0u, 0u, 0u);
-          if (p.bias != nullptr && n + 8 * g < p.N) b = __ldg(reinterpret_cast<const uint4*>(p.bias + n + 8 * g));
+          if (p.bias != nullptr && n + 8 * g < p.N) b = ld_bias<kMx4>(reinterpret_cast<const uint4*>(p.bias + n + 8 * g));
           const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
           if constexpr (kRow) {
             // row-wise FP8: y = fl(s_a[row] * s_b[n]) * acc + bias
@@ -1021,7 +1028,7 @@ __global__ void __launch_bounds__(Cfg<kCG, kBN, kAcc, kMx, kRow, kW16, kMx4>::kT
           v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
         }
         uint4 bv = make_uint4(0u, 0u, 0u, 0u);
-        if (p.bias != nullptr) bv = __ldg(reinterpret_cast<const uint4*>(p.bias + n));
+        if (p.bias != nullptr) bv = ld_bias<kMx4>(reinterpret_cast<const uint4*>(p.bias + n));
         const uint4 o = make_uint4(pack_bf16x2(fmaf(alpha, v[0], bf16_lo(bv.x)), fmaf(alpha, v[1], bf16_hi(bv.x))),
                                    pack_bf16x2(fmaf(alpha, v[2], bf16_lo(bv.y)), fmaf(alpha, v[3], bf16_hi(bv.y))),
                                    pack_bf16x2(fmaf(alpha, v[4], bf16_lo(bv.z)), fmaf(alpha, v[5], bf16_hi(bv.z))),

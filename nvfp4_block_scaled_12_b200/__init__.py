@@ -322,18 +322,12 @@ def nvfp4_last_error() -> str:
 # --------------------------------------------------------------------------
 
 _torch_module = None
-_empty_strided_cuda = None  # torch's allocation on the current device without the argument parsing (0.8 us, not 2)
 
 
 def _torch():
-    global _torch_module, _empty_strided_cuda  # (an import statement on every call costs more than the lookup)
+    global _torch_module  # (an import statement on every call costs more than the lookup)
     if _torch_module is None:
         import torch
-        if torch.cuda.is_available():
-            try:
-                from torch._C._dynamo.guards import _empty_strided_cuda
-            except ImportError:  # (not in every torch: Tensor.new_empty instead)
-                pass
         _torch_module = torch
     return _torch_module
 
@@ -734,21 +728,48 @@ def _like(stream, t):
     """A contiguous new tensor of the heads tensor ``t``'s shape and type, owned
     by the stream that writes it, and its nvfp4_heads."""
     b, l, h, d = t.shape
-    if stream is None and _empty_strided_cuda is not None:
-        out = _empty_strided_cuda((b, l, h, d), (l * h * d, h * d, d, 1), t.dtype)
-    else:
-        out = _empty_on(stream, (b, l, h, d), t, t.dtype)
+    out = _empty_on(stream, (b, l, h, d), t, t.dtype)
     return out, _HEADS.pack(out.data_ptr(), l * h * d, h * d, d)
 
 
+_direct_empty = None  # torch's allocation without the argument parsing (0.8 us, not 2); False: not to be had
+_dispatch_modes = None  # the number of dispatch modes that are active
+
+
+def _find_direct_empty():
+    """Looks for that allocation, which is none of torch's public names: used
+    only if it is there and a first tensor of it is what was asked for."""
+    global _direct_empty, _dispatch_modes
+    torch = _torch()
+    try:
+        from torch._C import _len_torch_dispatch_stack as modes
+        from torch._C._dynamo.guards import _empty_strided_cuda as empty
+        t = empty((3, 2), (2, 1), torch.uint8)
+        good = (type(t) is torch.Tensor and t.shape == (3, 2) and t.stride() == (2, 1) and t.dtype is torch.uint8
+                and t.get_device() == torch.cuda.current_device() and type(modes()) is int)
+    except Exception:
+        good = False
+    if good:
+        _dispatch_modes = modes
+    _direct_empty = empty if good else False
+    return _direct_empty
+
+
 def _empty_on(stream, shape, like, dtype):
-    """A new tensor on ``like``'s, the current device, owned by the stream that writes it."""
-    if stream is None:
-        if _empty_strided_cuda is not None and len(shape) <= 2:
-            return _empty_strided_cuda(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
+    """A new contiguous tensor on ``like``'s, the current device, owned by the stream that writes it."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return like.new_empty(shape, dtype=dtype)
+    direct = _find_direct_empty() if _direct_empty is None else _direct_empty
+    if direct is False or _dispatch_modes():  # (a dispatch mode is to see the allocation)
         return like.new_empty(shape, dtype=dtype)
-    with _torch().cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+    n = len(shape)
+    if n == 1:
+        return direct(shape, (1,), dtype)
+    if n == 2:
+        return direct(shape, (shape[1], 1), dtype)
+    _, l, h, d = shape
+    return direct(shape, (l * h * d, h * d, d, 1), dtype)
 
 
 def rope(q, positions, axes: Sequence[int], k=None, theta: float = 10000.0, q_weight=None, k_weight=None,

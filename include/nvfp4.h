@@ -436,7 +436,8 @@ nvfp4_status nvfp4_mxfp4_gemm(const uint8_t* a, const uint8_t* sfa, const uint8_
 /*
  * ------------------------------------------------------------------------
  * Between the linear layers of an attention block: rotary positions and
- * attention on 16-bit heads, as the GEMMs' epilogues write them.
+ * attention on 16-bit heads: bf16 as the GEMMs' epilogues write them and the
+ * quantizers read them, or fp16 (which the linear layers do not take).
  * ------------------------------------------------------------------------
  */
 enum { NVFP4_DTYPE_BF16 = 0, NVFP4_DTYPE_FP16 = 1 };
@@ -456,8 +457,9 @@ enum { NVFP4_ROPE_INTERLEAVED = 1, NVFP4_ROPE_SHARED_LADDER = 2 };
 
 /* One tensor to rotate.  out may be in itself (in place, with in's strides), or
  * must not overlap it; neither may overlap what the other tensor of the call
- * writes.  No two elements of an out share an address.  norm_weight [head_dim] (of the tensor's type) or NULL: with it, each
- * head is first divided by its root mean square and multiplied by the weight. */
+ * writes.  No two elements of an out share an address.  norm_weight [head_dim]
+ * (of the tensor's type) or NULL: with it, each head is first divided by its
+ * root mean square and multiplied by the weight. */
 typedef struct {
   nvfp4_heads in, out;
   int64_t heads;
@@ -623,8 +625,9 @@ nvfp4_status nvfp4_testing_set_grid_wait(uint64_t limit_ns, uint32_t extra_arriv
 /*
  * Launch shapes the library picks, for callers that size work around them
  * and for tests (host only: nothing touches a device).  Every GEMM entry point
- * (NVFP4, fused, dynamic, MXFP8, row-wise FP8) takes the same tile shape for
- * the same M, N and SM count:
+ * (NVFP4, fused, dynamic, MXFP4, MXFP8, row-wise FP8) takes the same tile shape
+ * for the same M, N and SM count, the ones that can split K as long as they do
+ * not (nvfp4_gemm_plan):
  *   out[0] = CTAs per output tile (1, or 2 for a CTA pair),
  *   out[1] = tile width in output columns (128, 192 or 256),
  *   out[2] = accumulator buffers in TMEM (1 or 2);
@@ -638,15 +641,15 @@ nvfp4_status nvfp4_gemm_tile_shape(int64_t M, int64_t N, int32_t num_sms, int32_
 
 /*
  * Launch plan of the GEMMs with the plain epilogue -- nvfp4_gemm,
- * nvfp4_gemm_scaled, nvfp4_gemm_dynamic, nvfp4_gemm_amax (w4a16 = 0) and nvfp4_w4a16_gemm
- * (w4a16 = 1) -- for an M x N x K problem on num_sms SMs (host only):
+ * nvfp4_gemm_scaled, nvfp4_gemm_dynamic, nvfp4_gemm_amax, nvfp4_mxfp4_gemm
+ * (w4a16 = 0) and nvfp4_w4a16_gemm (w4a16 = 1) -- for an M x N x K problem on num_sms SMs (host only):
  *   out[0..2] = tile shape as nvfp4_gemm_tile_shape reports it,
  *   out[3]    = K split: tile groups (CTAs or CTA pairs) that share one
  *               output tile over disjoint ranges of k-tiles (1, 2 or 4).
  * When the tiles cannot fill the SMs (a few hundred tokens or fewer) and K is
  * long enough for the split to pay for its own work, up to 4 CTAs of a
  * thread-block cluster work on one tile, each over its own k-tile range
- * (k-tiles of 256 elements for NVFP4, 64 for W4A16), and sum their fp32
+ * (k-tiles of 256 elements for NVFP4 and MXFP4, 64 for W4A16), and sum their fp32
  * partial tiles through distributed shared memory in a fixed order before the
  * epilogue (so results are deterministic; they may differ from the unsplit
  * sum in the last bits, within the GEMM's tolerance).  The shape is then the
@@ -658,7 +661,7 @@ nvfp4_status nvfp4_gemm_plan(int64_t M, int64_t N, int64_t K, int32_t num_sms, i
                              int32_t* out);
 
 /*
- * Rows per tile of the NVFP4 and MXFP8 quantizers for an [M, K] input on a
+ * Rows per tile of the NVFP4, MXFP4 and MXFP8 quantizers for an [M, K] input on a
  * device with num_sms SMs: 256 once every SM gets at least eight 256-row
  * tiles of 64 columns, else 128.  0 for invalid sizes (M or K out of range,
  * K not a multiple of 64, num_sms < 1).  Host only.

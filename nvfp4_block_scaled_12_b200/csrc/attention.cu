@@ -46,10 +46,13 @@
 // products), the exponentials' 2048 (16 a clock and SM); a step takes 3300.  The
 // softmax warps are busy for 2560 to 2930 of them: those that share a scheduler
 // with an MMA issuer are the slow ones.  Joint attention of 4608 tokens, 24 heads
-// of 128: 200 us back to back = 1.31 PFLOP/s (0.79 of the measured bf16 burst;
-// under the power cap 236); heads of 64: 180 us (113 are the exponentials' floor);
-// 4096 queries over 512 and 382 states, 24 heads of 128: 57 us, a quarter of it
-// between items.
+// of 128: 200 to 205 us back to back = 1.27 to 1.31 PFLOP/s (0.79 of the measured
+// bf16 burst; under the power cap 236); heads of 64: 179 us (113 are the exponentials' floor);
+// 4096 queries over 512 and 382 states, 24 heads of 128: 57 us.  There a step takes
+// 1.7 us and an item's two ends, which nothing covers, 2.3; and the 768 items in
+// turns of 148 leave 28 CTAs a sixth one, 21 key tiles in all against 17 or 18: by
+// these figures 49.5 us for the longest CTA and 42.8 for the average one, so about
+// 7 us pass with four fifths of the SMs done.
 // Measured and not kept: a share of the exponentials as a cubic on the FMA pipes
 // (no gain at any share), two threads a row (a vote a tile: the same speed), an
 // output warpgroup of its own (206 us), P handed over in halves.
@@ -69,12 +72,12 @@
 // joined within the CTA before the ranks join (a row that an infinite V turned
 // into NaN that way is made once more, few_rows_again).  A tile then costs its two
 // products, 0.57 us, instead of 1.05, and the ring has six stages for four.  One
-// query over 16384, 14334, 12284 and 10239 states, 32 heads on 8 of 128: 43.4 us
-// (218 MB: 5.0 TB/s) against 50.5; what is left is that the longest entry's CTAs end
-// last (2 to 3 us) and 9 us of start, join and end.  32 entries of 4096 states each:
-// 87.5 us = 6.1 TB/s, 0.94 of a copy; short items pay their start and join (64
-// entries of 1024 states, 16 heads of 64: 3.1 TB/s).  33 to 64 rows could have two
-// copies; they have none.
+// query over 16384, 14334, 12284 and 10239 states, 32 heads on 8 of 128: 41.5 us
+// (218 MB: 5.3 TB/s); what is left is that the longest entry's CTAs end last (2 to 3
+// us) and 6 us of start, join and end.  32 entries of 4096 states each: 84.7 us =
+// 6.3 TB/s, 0.97 of a copy; short items pay their start and join (64 entries of 1024
+// states, 16 heads of 64: 3.2 TB/s).  33 to 64 rows could have two copies; they have
+// none.
 #include "internal.h"
 
 namespace nvfp4 {

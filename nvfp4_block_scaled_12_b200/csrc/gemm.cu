@@ -1139,6 +1139,14 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int num_kt, int num_sms) {
   // resident at once (at most 7/8 of the SMs: clusters of 4 CTAs with this
   // kernel's shared memory fit 33 at a time on 148 SMs, of 8 only 15), and at
   // least one k-tile to a range.
+  // The figures are NVFP4's; MXFP4 takes the same rule.  Measured on MXFP4 (GEMM
+  // alone, us, N x K = 3072 x 3072; split 1 / 2 / 4 of the shape for M <= 128):
+  // M = 1 8.2 / 7.1 / 6.5, M = 64 8.2 / 9.4 / 9.4, M = 128 8.4 / 10.0 / 10.8, so the
+  // split of 4 that it takes gains 1.7 at one row and costs 1.2 and 2.4 at 64 and
+  // 128 (the reduction grows with the rows).  M = 512, K = 4608: 2 x 256 x 192 tiles
+  // split in two 12.4, 256 x 128 whole 10.1.  M = 4608, N = 12288: wide tiles 77,
+  // 256 x 192 95, 256 x 128 117; M = 1500: wide tiles, 72 for the threshold's
+  // 74, 10.4 against 13.7 of the 256 x 192 it takes.
   constexpr int64_t kSplitCost = 6;
   auto cost = [&](const GemmConfig& c, int* ks_out) {
     const int64_t groups = num_sms / c.cta_group;

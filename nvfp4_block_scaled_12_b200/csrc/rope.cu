@@ -13,8 +13,10 @@
 // and cosines are worked out once for all of them and a row's norm is a shuffle
 // within the group.  Lanes load the next four heads before they use the last
 // four, 16 bytes each (two 8-byte halves in the half layout), and four blocks
-// fit an SM.  4608 tokens x 48 heads x 128 with the norms: 18.6 us back to back
-// (6.1 TB/s, 0.93 of a copy); 30940 tokens x 24 heads x 128: 59.9 us (6.3 TB/s, 0.97).
+// fit an SM.  30940 tokens x 24 heads x 128: 59.9 us (380 MB: 6.3 TB/s, 0.97 of a
+// copy).  4608 tokens x 48 heads x 128 (113 MB) over six sets of buffers, more than
+// the L2 holds: 20.4 us (5.5 TB/s, 0.85), with the norms 22.5 (5.0 TB/s, 0.77);
+// on one set of buffers, which the L2 mostly holds, 15.8 and 18.0.
 //
 // The angle is reduced in 64 bits: t = pos * (f_i / 2 pi) turns, of which only
 // t - rint(t) goes on in 32 bits, so a position of a million costs no accuracy
@@ -241,8 +243,14 @@ bool rope_plan(RopeParams* p, int64_t tokens, int num_sms, int64_t* blocks) {
   p->inv_d = 1.0f / static_cast<float>(p->D);
   // Heads of one unit: up to 24 share their sines and cosines where that leaves
   // every SM two blocks' worth of units, fewer where the units would be too few
-  // to keep the memory busy.  (At most 24 / 12 / 8 / 6 heads: 24.8 / 24.7 / 26.8 /
-  // 33 us for 48 heads of 4608 tokens, L2-cold 26.7 / 28.7 / 30.8 / 34.8.)
+  // to keep the memory busy.  At most 24 / 12 / 6 / 3 heads, in us, call after call:
+  //   48 heads x 4608 tokens with norms, in the L2    18.0 / 19.2 / 26.4 / 34.2
+  //                                     beyond it     22.5 / 20.5 / 26.5 / 34.3
+  //                          no norms,  in the L2     15.8 / 16.9 / 20.5 / 26.1
+  //                                     beyond it     20.4 / 19.7 / 21.2 / 26.3
+  //   24 heads x 30940 tokens, no norms               60.1 / 58.3 / 64.7 / 82.9
+  // 24 is the best where the projection has just left Q and K in the L2, 12 (two
+  // waves of half the work) by 1 to 2 us where everything comes from memory.
   for (int most = 24;; most /= 2) {
     int parts[2] = {0, 0};
     p->heads_per_unit = 0;

@@ -876,6 +876,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             any = true;
           }
         }
+        __syncwarp();
         if (__builtin_expect(named_barrier_any(2, 256, any), 0))
           few_rows_again<kDP, kFp16, C>(p, first, rank, *again, part);
       }

@@ -109,3 +109,42 @@ def test_infinities_seen_from_a_replayed_graph(F):
     graph.replay()
     torch.cuda.synchronize()
     _check(out, q, k, v)
+
+
+@pytest.mark.parametrize("layout", ["heads before tokens", "fused columns", "shared by the batch"])
+@pytest.mark.parametrize("D,dtype", [(64, HF), (120, BF)])
+def test_infinities_in_views(F, layout, D, dtype):
+    # the rows that are made once more are read by plain loads with the tensors' own strides
+    B, Lq, Lk, Hq, Hk = 3, 4, 1200, 6, 3
+    if layout == "heads before tokens":
+        q = _rand((B, Hq, Lq, D + 8), dtype, 140)[..., :D].transpose(1, 2)
+        k, v = (_rand((B, Hk, Lk, D + 8), dtype, s)[..., :D].transpose(1, 2) for s in (141, 142))
+    elif layout == "fused columns":
+        q = _rand((B, Lq, (Hq + 1) * D), dtype, 143)[..., D:].unflatten(2, (Hq, D))
+        k, v = _rand((B, Lk, 2, Hk, D), dtype, 144).unbind(2)
+    else:
+        q = _rand((1, Lq, Hq, D), dtype, 145).expand(B, -1, -1, -1)
+        k, v = (_rand((1, Lk, Hk, D), dtype, s).expand(B, -1, -1, -1) for s in (146, 147))
+    v[0, 700, 1, D - 1] = INF
+    v[-1, 701, 2, 0] = -INF
+    lens = torch.tensor([1200, 0, 702], dtype=torch.int32).cuda()
+    store = torch.full((B, Lq, Hq, D + 8), 7.0, device="cuda", dtype=dtype)
+    F.cross_attention(q, k, v, kv_lens=lens, out=store[..., :D])
+    _check_classes(store[..., :D].contiguous(), q, k, v.clone(), lens)
+    assert bool((store[..., D:] == 7.0).all()) and bool((store[1, ..., :D] == 0).all())
+
+
+def test_infinities_on_several_streams_at_once(F):
+    sets = [[_rand((2, n, 4, 64), BF, 150 + 10 * i + n) for n in (1, 2000, 2000)] for i in range(4)]
+    for i, (_, _, v) in enumerate(sets):
+        v[i % 2, 100 * i, i, 2 * i] = INF
+    want = [F.cross_attention(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[F.cross_attention(*s, stream=stream) for _ in range(5)] for s, stream in zip(sets, streams)]
+    torch.cuda.synchronize()
+    for s, w, gs in zip(sets, want, got):
+        _check_classes(w, *s)
+        assert all(torch.equal(w.view(torch.int16), x.view(torch.int16)) for x in gs)
+    F.nvfp4_check_fault()
